@@ -286,6 +286,95 @@ int moe_forward_decode_static(const moe_shape* shape, const uint16_t* x_dev, con
                               const void* packed_shared_dev, const moe_routing* routing, uint16_t* y_dev,
                               void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * A gate over given router logits, and the dense projections beside the experts.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Element types of the calls below. */
+#define MOE_F32 0
+#define MOE_BF16 1
+#define MOE_F16 2
+
+/* moe_gate_config.score */
+#define MOE_SCORE_SOFTMAX 0   /* softmax over the E logits */
+#define MOE_SCORE_SIGMOID 1   /* 1 / (1 + exp(-logit)), each expert on its own */
+/* moe_gate_config.group_score */
+#define MOE_GROUP_TOP2 0      /* a group is worth the sum of its two largest choice values */
+#define MOE_GROUP_MAX 1       /* a group is worth its largest choice value */
+
+/* A gate: which k of E experts each token goes to, and with which weights.
+ *   s = score(logits); choice value v = s + select_bias (s without a bias);
+ *   with groups > 1 the E experts form `groups` runs of E / groups consecutive experts, and only
+ *   the group_topk groups of the highest worth (group_score) can be chosen from;
+ *   the k largest v are chosen (slots in rank order), weights w = s of the chosen (without the
+ *   bias), renormalise: divided by their sum, then times scale.
+ * Ties, of experts and of groups, go to the lower index.  A NaN logit counts as -inf, +inf as
+ * the largest finite number; a NaN choice value as -inf.  -inf switches an expert off: its score
+ * is 0.  A token whose k chosen scores sum to 0 (every expert switched off) gets the lowest
+ * indices of equal choice values and weights of 0, renormalised or not. */
+typedef struct moe_gate_config {
+    int T, E, k;               /* 0 <= T <= 2^20, 1 <= E <= 1024, 1 <= k <= min(32, E) */
+    int logits_type;           /* MOE_F32, MOE_BF16 or MOE_F16 */
+    int score;                 /* MOE_SCORE_* */
+    int groups, group_topk;    /* groups 0 or 1: no groups.  Else 2..32 groups, E % groups == 0,
+                                  1 <= group_topk <= groups, k <= group_topk * E / groups, and
+                                  E / groups >= 2 for MOE_GROUP_TOP2 */
+    int group_score;           /* MOE_GROUP_* */
+    int renormalise;           /* 0 or 1 */
+    float scale;               /* finite */
+    long long logits_stride;   /* elements from one token's logits to the next; 0: E */
+} moe_gate_config;
+
+/* logits_dev [T] rows of E (rows of any stride >= E), select_bias_dev fp32 [E] or null ->
+ * topk_idx_dev int32 [T][k], topk_w_dev fp32 [T][k], the layouts of moe_routing.  Scores and
+ * choice values are fp32 whatever the logits' type.  One launch, no workspace.  logits_dev must be
+ * aligned to its element size (16 bytes are faster), the others to 4 bytes. */
+int moe_gate(const moe_gate_config* config, const void* logits_dev, const float* select_bias_dev,
+             int32_t* topk_idx_dev, float* topk_w_dev, void* stream);
+
+/* Steps a3-a6 for a choice that is already there: routing->topk_idx_dev and topk_w_dev [T][8]
+ * (written by moe_gate or by any gate) -> counts, offsets, perm, pos, block map, and the token rows
+ * gathered into expert order inside the workspace, as moe_route leaves them for moe_grouped_ffn.
+ * x_dev [T][d] bf16.  A token's 8 experts must differ and lie in [0, 256): an index outside sets
+ * MOE_STATUS_BAD_EXPERT and that row is left out.  moe_options.host_routing is not taken here
+ * (MOE_ERR_UNSUPPORTED); the other options as in moe_route. */
+int moe_dispatch(const moe_shape* shape, const uint16_t* x_dev, const moe_routing* routing, void* workspace_dev,
+                 size_t workspace_bytes, const moe_options* options, void* stream);
+
+/* moe_linear_config.activation */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2        /* z / (1 + exp(-z)) */
+#define MOE_ACT_GELU 3        /* z * Phi(z), Phi the normal distribution (erf) */
+#define MOE_ACT_GELU_TANH 4   /* the tanh form of GELU */
+#define MOE_ACT_SWIGLU 5      /* w holds 2N rows, N of the gate then N of the up projection:
+                                 silu(gate) * up */
+
+/* y = act(x w^T + bias) + residual with x [T][K], w [N][K] (2N rows for MOE_ACT_SWIGLU), one
+ * rounding from fp32 to y's type at the end.  Strides are elements from row to row (0: dense rows). */
+typedef struct moe_linear_config {
+    int T, N, K;               /* 0 <= T <= 2^20, 1 <= N <= 2^20, 1 <= K <= 65536 */
+    int type;                  /* of x and w: MOE_BF16 or MOE_F16 */
+    int out_type;              /* of y and residual: type, or MOE_F32 */
+    int activation;            /* MOE_ACT_* */
+    long long x_stride, w_stride, residual_stride, y_stride;
+} moe_linear_config;
+
+/* Bytes of the workspace of moe_linear for this config (0 if it is unsupported): a status word
+ * (zero the workspace once before first use; moe_read_status reads it) and, when a row of x or w does
+ * not start at a multiple of 16 bytes (stride % 8 != 0), room for an aligned copy of that operand.
+ * One workspace serves one stream at a time. */
+size_t moe_linear_workspace_bytes(const moe_linear_config* config);
+
+/* bias_dev fp32 [N] ([2N] for MOE_ACT_SWIGLU) or null, residual_dev [T][N] of out_type or null.
+ * Products are accumulated in fp32; for an fp32 y partial sums of at most 512 products go through
+ * the tensor cores' accumulator before they are added in ordinary fp32.  Results do not depend on
+ * the run (no atomics).  x, w and the workspace must be 16- and 256-byte aligned as
+ * everywhere here, y and residual to 16 bytes, bias to 4.  y may be residual itself (same pointer and stride); else
+ * y must not overlap an input. */
+int moe_linear(const moe_linear_config* config, const void* x_dev, const void* w_dev, const float* bias_dev,
+               const void* residual_dev, void* y_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

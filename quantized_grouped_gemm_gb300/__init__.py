@@ -6,7 +6,8 @@ as ``torch.bfloat16`` or as 16-bit integer tensors holding the bit patterns.
 
 Calls have the names of the C ABI: ``moe_route``, ``moe_grouped_ffn`` (= ``moe_ffn_gate_up``
 then ``moe_ffn_down``), ``moe_combine``, ``moe_forward``, ``moe_pack_weights``,
-``moe_read_status``.
+``moe_read_status``; ``moe_gate`` and ``moe_dispatch`` (any gate in place of the router's own
+choice) and ``moe_linear`` (the unquantised projections beside the experts).
 """
 from __future__ import annotations
 
@@ -22,7 +23,8 @@ from ._lib import (MOE_ERR_CUDA, MOE_ERR_DEVICE_STATUS, MOE_ERR_DEVICE_TIMEOUT, 
 __all__ = ["MoEError", "shape", "options", "Routing", "workspace", "moe_workspace_bytes", "moe_packed_bytes",
            "moe_pack_weights", "moe_route", "moe_grouped_ffn", "moe_ffn_gate_up", "moe_ffn_down", "moe_combine",
            "moe_forward", "moe_read_status", "moe_check_shape", "moe_launch_count", "moe_forward_decode_static",
-           "lib"]
+           "gate_config", "moe_gate", "moe_dispatch", "linear_config", "linear_workspace",
+           "moe_linear_workspace_bytes", "moe_linear", "lib"]
 
 
 class MoEError(RuntimeError):
@@ -194,3 +196,60 @@ def moe_read_status(ws, stream=None):
     bits = ctypes.c_int(0)
     rc = lib().moe_read_status(_p(ws), _s(stream), ctypes.byref(bits))
     return rc, bits.value
+
+
+_TYPES = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16, torch.float16: _lib.MOE_F16}
+_SCORES = {"softmax": _lib.MOE_SCORE_SOFTMAX, "sigmoid": _lib.MOE_SCORE_SIGMOID}
+_GROUP_SCORES = {"top2": _lib.MOE_GROUP_TOP2, "max": _lib.MOE_GROUP_MAX}
+_ACTIVATIONS = {"none": _lib.MOE_ACT_NONE, "relu": _lib.MOE_ACT_RELU, "silu": _lib.MOE_ACT_SILU,
+                "gelu": _lib.MOE_ACT_GELU, "gelu_tanh": _lib.MOE_ACT_GELU_TANH, "swiglu": _lib.MOE_ACT_SWIGLU}
+
+
+def gate_config(T: int, E: int = 256, k: int = 8, score: str = "softmax", dtype: torch.dtype = torch.float32,
+                groups: int = 1, group_topk: int = 1, group_score: str = "top2", renormalise: bool = True,
+                scale: float = 1.0, logits_stride: int = 0) -> _lib.moe_gate_config:
+    """The gate of moe_gate (see moe_gate_config in moe.h): score "softmax" or "sigmoid", group_score
+    "top2" or "max", dtype that of the logits, logits_stride in elements (0: E)."""
+    return _lib.moe_gate_config(T, E, k, _TYPES[dtype], _SCORES[score], groups, group_topk, _GROUP_SCORES[group_score],
+                                int(renormalise), scale, logits_stride)
+
+
+def moe_gate(cfg, logits, select_bias, topk_idx, topk_w, stream=None) -> None:
+    """The k experts and weights of every token, into topk_idx (int32) and topk_w (fp32) [T, k]."""
+    _check(lib().moe_gate(ctypes.byref(cfg), _p(logits), _p(select_bias), _p(topk_idx), _p(topk_w), _s(stream)),
+           "moe_gate")
+
+
+def moe_dispatch(shp, x, routing: Routing, ws, opts=None, stream=None) -> None:
+    """The routing metadata and gathered rows for the choice in routing.topk_idx / topk_w."""
+    _check(lib().moe_dispatch(ctypes.byref(shp), _p(x), routing.ref(), _p(ws), ws.numel(), _o(opts), _s(stream)),
+           "moe_dispatch")
+
+
+def linear_config(T: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16,
+                  out_dtype: Optional[torch.dtype] = None, activation: str = "none", x_stride: int = 0,
+                  w_stride: int = 0, residual_stride: int = 0, y_stride: int = 0) -> _lib.moe_linear_config:
+    """The projection of moe_linear (see moe_linear_config in moe.h): dtype of x and w, out_dtype of y and
+    residual (default: dtype), strides in elements (0: dense rows)."""
+    return _lib.moe_linear_config(T, N, K, _TYPES[dtype], _TYPES[dtype if out_dtype is None else out_dtype],
+                                  _ACTIVATIONS[activation], x_stride, w_stride, residual_stride, y_stride)
+
+
+def moe_linear_workspace_bytes(cfg) -> int:
+    return int(lib().moe_linear_workspace_bytes(ctypes.byref(cfg)))
+
+
+def linear_workspace(cfg, device="cuda") -> torch.Tensor:
+    """A workspace for moe_linear (its status word zeroed)."""
+    n = moe_linear_workspace_bytes(cfg)
+    if n == 0:
+        raise MoEError("moe_linear_workspace_bytes", MOE_ERR_UNSUPPORTED)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def moe_linear(cfg, x, w, bias, residual, y, ws, stream=None) -> None:
+    """y = act(x w^T + bias) + residual; bias (fp32) and residual may be None, y may be residual."""
+    _check(lib().moe_linear(ctypes.byref(cfg), _p(x), _p(w), _p(bias), _p(residual), _p(y), _p(ws), ws.numel(),
+                            _s(stream)), "moe_linear")

@@ -20,6 +20,10 @@ MOE_ERR_WORKSPACE = -6
 MOE_STATUS_BAD_EXPERT = 0x1
 MOE_STATUS_TIMEOUT = 0x2
 MOE_STATIC_SCRATCH_BYTES = 131072
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_TOP2, MOE_GROUP_MAX = 0, 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SWIGLU = range(6)
 
 _P = ctypes.c_void_p
 
@@ -48,6 +52,20 @@ class moe_options(ctypes.Structure):
                 ("unfused_dequant", ctypes.c_int), ("gemm_rows", ctypes.c_int), ("reserved", ctypes.c_int * 1)]
 
 
+class moe_gate_config(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("E", ctypes.c_int), ("k", ctypes.c_int), ("logits_type", ctypes.c_int),
+                ("score", ctypes.c_int), ("groups", ctypes.c_int), ("group_topk", ctypes.c_int),
+                ("group_score", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float),
+                ("logits_stride", ctypes.c_longlong)]
+
+
+class moe_linear_config(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("type", ctypes.c_int),
+                ("out_type", ctypes.c_int), ("activation", ctypes.c_int), ("x_stride", ctypes.c_longlong),
+                ("w_stride", ctypes.c_longlong), ("residual_stride", ctypes.c_longlong),
+                ("y_stride", ctypes.c_longlong)]
+
+
 _SPS = ctypes.POINTER(moe_shape)
 _SIG = {
     "moe_error_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -73,6 +91,11 @@ _SIG = {
     "moe_read_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_int)]),
     "moe_launch_count": (ctypes.c_ulonglong, []),
     "moe_forward_decode_static": (ctypes.c_int, [_SPS, _P, _P, _P, _P, _P, ctypes.POINTER(moe_routing), _P, _P]),
+    "moe_gate": (ctypes.c_int, [ctypes.POINTER(moe_gate_config), _P, _P, _P, _P, _P]),
+    "moe_dispatch": (ctypes.c_int, [_SPS, _P, ctypes.POINTER(moe_routing), _P, ctypes.c_size_t,
+                                    ctypes.POINTER(moe_options), _P]),
+    "moe_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_linear_config)]),
+    "moe_linear": (ctypes.c_int, [ctypes.POINTER(moe_linear_config), _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
 }
 
 _lib = None

@@ -2,6 +2,7 @@
 // layout, tensor maps and kernel launches.  Nothing here allocates device memory or
 // synchronises a stream (except moe_read_status, a debug call).
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "moe_internal.cuh"
@@ -410,6 +411,111 @@ int moe_forward(const moe_shape* s, const uint16_t* x, const uint16_t* w_router,
     rc = moe_grouped_ffn(s, x, rt, wr, wsh, ws, ws_bytes, o, stream);
     if (rc != MOE_OK) return rc;
     return moe_combine(s, rt, ws, ws_bytes, y, o, stream);
+}
+
+int moe_gate(const moe_gate_config* c, const void* logits, const float* bias, int32_t* idx, float* w, void* stream) {
+    if (!c || c->T < 0 || c->E <= 0 || c->k <= 0 || c->groups < 0 || c->logits_stride < 0) return MOE_ERR_INVALID_ARG;
+    if (c->logits_type < MOE_F32 || c->logits_type > MOE_F16 || (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) ||
+        (c->group_score != MOE_GROUP_TOP2 && c->group_score != MOE_GROUP_MAX) || (c->renormalise != 0 && c->renormalise != 1) ||
+        !std::isfinite(c->scale))
+        return MOE_ERR_INVALID_ARG;
+    const int groups = c->groups == 0 ? 1 : c->groups;
+    if (c->T > (1 << 20) || c->E > 1024 || c->k > 32 || groups > 32) return MOE_ERR_UNSUPPORTED;
+    if (c->k > c->E || (c->logits_stride != 0 && c->logits_stride < c->E)) return MOE_ERR_INVALID_ARG;
+    if (groups > 1) {
+        if (c->E % groups != 0 || c->group_topk < 1 || c->group_topk > groups ||
+            c->k > c->group_topk * (c->E / groups) || (c->group_score == MOE_GROUP_TOP2 && c->E / groups < 2))
+            return MOE_ERR_INVALID_ARG;
+    }
+    if (c->T == 0) return MOE_OK;
+    const size_t size = c->logits_type == MOE_F32 ? 4 : 2;
+    if (!logits || !idx || !w || !aligned(logits, size) || !aligned(idx, 4) || !aligned(w, 4) ||
+        (bias && !aligned(bias, 4)))
+        return MOE_ERR_INVALID_ARG;
+    GateArgs a{};
+    a.T = c->T; a.E = c->E; a.k = c->k;
+    a.groups = groups; a.group_topk = c->group_topk;
+    a.sigmoid = c->score == MOE_SCORE_SIGMOID;
+    a.group_max = c->group_score == MOE_GROUP_MAX;
+    a.renormalise = c->renormalise == 1;
+    a.scale = c->scale;
+    a.logits = logits;
+    a.stride = c->logits_stride == 0 ? c->E : c->logits_stride;
+    a.vec = aligned(logits, 16) && (a.stride * (long long)size) % 16 == 0;
+    a.bias = bias; a.topk_idx = idx; a.topk_w = w;
+    unsigned long long n = 0;
+    const cudaError_t e = launch_gate(a, c->logits_type, static_cast<cudaStream_t>(stream), &n);
+    g_launches += n;
+    return cuda_status(e);
+}
+
+int moe_dispatch(const moe_shape* s, const uint16_t* x, const moe_routing* rt, void* ws, size_t ws_bytes,
+                 const moe_options* o, void* stream) {
+    int rc = moe_check_shape(s);
+    if (rc != MOE_OK) return rc;
+    Opts op;
+    if ((rc = get_opts(o, &op)) != MOE_OK) return rc;
+    if (op.host_routing) return MOE_ERR_UNSUPPORTED;
+    if (s->T == 0) return MOE_OK;
+    if ((rc = check_routing(rt)) != MOE_OK) return rc;
+    if ((rc = check_ws(s, ws, ws_bytes, op)) != MOE_OK) return rc;
+    if (!x || !aligned(x, 16)) return MOE_ERR_INVALID_ARG;
+    const RouteArgs a = route_args(s, x, nullptr, nullptr, rt, ws, op);
+    unsigned long long n = 0;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = is_decode(s, op) ? launch_dispatch_decode(a, st, &n) : launch_dispatch_prefill(a, st, &n);
+    g_launches += n;
+    return cuda_status(e);
+}
+
+// Checks a config and fills the sizes and strides of the kernels' arguments.
+static int linear_args(const moe_linear_config* c, LinearArgs* a) {
+    if (!c || c->T < 0 || c->N <= 0 || c->K <= 0) return MOE_ERR_INVALID_ARG;
+    if ((c->type != MOE_BF16 && c->type != MOE_F16) || (c->out_type != c->type && c->out_type != MOE_F32) ||
+        c->activation < MOE_ACT_NONE || c->activation > MOE_ACT_SWIGLU)
+        return MOE_ERR_INVALID_ARG;
+    if (c->T > (1 << 20) || c->N > (1 << 20) || c->K > 65536) return MOE_ERR_UNSUPPORTED;
+    const long long strides[4] = {c->x_stride, c->w_stride, c->residual_stride, c->y_stride};
+    const int widths[4] = {c->K, c->K, c->N, c->N};
+    for (int i = 0; i < 4; ++i) {
+        if (strides[i] != 0 && strides[i] < widths[i]) return MOE_ERR_INVALID_ARG;
+        if (strides[i] > (1ll << 36)) return MOE_ERR_UNSUPPORTED;   // a tensor map's row pitch ends at 2^40 bytes
+    }
+    a->T = c->T; a->N = c->N; a->K = c->K;
+    a->rows = c->activation == MOE_ACT_SWIGLU ? 2 * c->N : c->N;
+    a->act = c->activation;
+    a->f16 = c->type == MOE_F16;
+    a->out_f32 = c->out_type == MOE_F32;
+    a->x_stride = strides[0] ? strides[0] : c->K;
+    a->w_stride = strides[1] ? strides[1] : c->K;
+    a->r_stride = strides[2] ? strides[2] : c->N;
+    a->y_stride = strides[3] ? strides[3] : c->N;
+    a->num_sms = num_sms();
+    return MOE_OK;
+}
+
+size_t moe_linear_workspace_bytes(const moe_linear_config* c) {
+    LinearArgs a{};
+    return linear_args(c, &a) == MOE_OK ? linear_workspace(a) : 0;
+}
+
+int moe_linear(const moe_linear_config* c, const void* x, const void* w, const float* bias, const void* residual,
+               void* y, void* ws, size_t ws_bytes, void* stream) {
+    LinearArgs a{};
+    const int rc = linear_args(c, &a);
+    if (rc != MOE_OK) return rc;
+    if (a.T == 0) return MOE_OK;
+    if (!x || !w || !y || !ws || !aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(ws, 256) ||
+        (bias && !aligned(bias, 4)) || (residual && !aligned(residual, 16)))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < linear_workspace(a)) return MOE_ERR_WORKSPACE;
+    if (a.num_sms <= 0) return MOE_ERR_CUDA;
+    a.x = x; a.w = w; a.bias = bias; a.residual = residual; a.y = y;
+    a.ws = static_cast<uint8_t*>(ws);
+    unsigned long long n = 0;
+    const cudaError_t e = launch_linear(a, static_cast<cudaStream_t>(stream), &n);
+    g_launches += n;
+    return cuda_status(e);
 }
 
 int moe_read_status(void* ws, void* stream, int* status_out) {

@@ -737,6 +737,42 @@ cudaError_t launch_pack(int E, int N, int K, const moe_q4& m, int pair_slot, int
 cudaError_t launch_scale_check(size_t n, const uint16_t* scales, int* mode, cudaStream_t st,
                                unsigned long long* launches);
 
+// moe_gate: one warp per token (gate.cu).
+struct GateArgs {
+    int T, E, k;
+    int groups, group_topk;
+    bool sigmoid, group_max, renormalise;
+    bool vec;                  // logits rows start at multiples of 16 bytes
+    float scale;
+    const void* logits;
+    long long stride;
+    const float* bias;
+    int32_t* topk_idx;
+    float* topk_w;
+};
+cudaError_t launch_gate(const GateArgs& a, int logits_type, cudaStream_t st, unsigned long long* launches);
+
+// moe_dispatch (route.cu): routing metadata for the choice in a.topk_idx / a.topk_w.
+cudaError_t launch_dispatch_prefill(const RouteArgs& a, cudaStream_t st, unsigned long long* launches);
+cudaError_t launch_dispatch_decode(const RouteArgs& a, cudaStream_t st, unsigned long long* launches);
+
+// moe_linear (linear.cu).  Strides in elements; w has `rows` = N or 2N rows.
+struct LinearArgs {
+    int T, N, K, rows;
+    int act;
+    bool f16, out_f32;
+    const void* x;
+    const void* w;
+    const float* bias;
+    const void* residual;
+    void* y;
+    long long x_stride, w_stride, r_stride, y_stride;
+    uint8_t* ws;
+    int num_sms;
+};
+size_t linear_workspace(const LinearArgs& a);
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st, unsigned long long* launches);
+
 // Encodes 2-D bf16 tensor maps (host; driver entry point fetched through the runtime).
 cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                               uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,

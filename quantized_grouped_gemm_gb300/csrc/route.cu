@@ -1159,6 +1159,117 @@ cudaError_t launch_route_prefill_host(const RouteArgs& a, cudaStream_t st, unsig
     return launch_with_pdl(route_scatter, dim3(nblk, a.k), dim3(256), 0, st, a);
 }
 
+namespace {
+// ---------------------------------------------------------------------------------------
+// route_count: the per-block expert counts that route_scan reads, for a choice made elsewhere
+// (moe_dispatch).  One CTA per 32-token block, a thread per assignment; a token whose slots name
+// one expert twice counts once, as in route_scatter's bitmasks.  pos of an index outside [0, E)
+// (flagged by route_scatter) is set to 0, an existing row.
+// ---------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) route_count(RouteArgs a) {
+    __shared__ uint32_t s_mask[256];
+    s_mask[threadIdx.x] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    __syncthreads();
+    const int t = blockIdx.x * kRouteBlockTokens + threadIdx.x / 8;   // k == 8
+    if (t < a.T) {
+        const size_t q = (size_t)t * 8 + threadIdx.x % 8;
+        const int e = a.topk_idx[q];
+        if (e >= 0 && e < 256) atomicOr(&s_mask[e], 1u << (threadIdx.x / 8));
+        else a.pos[q] = 0;
+    }
+    __syncthreads();
+    reinterpret_cast<int32_t*>(a.ws + a.L.blk)[(size_t)blockIdx.x * 256 + threadIdx.x] = __popc(s_mask[threadIdx.x]);
+}
+
+// ---------------------------------------------------------------------------------------
+// dispatch_one: the metadata of a single token (T = 1) and the cleared accumulators, as
+// route_decode leaves them for the decode kernels.  One warp ranks the eight experts.
+// ---------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(1024) dispatch_one(RouteArgs a) {
+    __shared__ int s_e[8];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x;
+    if (tid < 8) {
+        const int e = a.topk_idx[tid];
+        if (e < 0 || e >= 256) set_status(reinterpret_cast<int*>(a.ws + a.L.status), MOE_STATUS_BAD_EXPERT);
+        s_e[tid] = e;
+    }
+    __syncthreads();
+    if (tid <= 256) {
+        int off = 0, cnt = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const bool in = s_e[q] >= 0 && s_e[q] < 256;
+            off += in && s_e[q] < tid;
+            cnt += in && s_e[q] == tid;
+        }
+        a.offsets[tid] = off;
+        if (tid < 256) {
+            a.counts[tid] = cnt;
+            // a group has one row (two only where the caller names an expert twice): its tiles
+            for (int r = 0, i = 0; r < cnt; r += a.tile_rows, ++i) {
+                int before = 0;   // tiles of the lower experts
+                for (int q = 0; q < 8; ++q) {
+                    bool first = s_e[q] >= 0 && s_e[q] < tid;
+                    int c = 0;
+                    for (int p = 0; p < 8; ++p) {
+                        first = first && !(p < q && s_e[p] == s_e[q]);
+                        c += s_e[p] == s_e[q];
+                    }
+                    if (first) before += (c + a.tile_rows - 1) / a.tile_rows;
+                }
+                int32_t* t = a.tiles + 3 * (size_t)(before + i);
+                t[0] = tid;
+                t[1] = off + r;
+                t[2] = min(a.tile_rows, cnt - r);
+            }
+        }
+    }
+    if (tid < 8) {
+        const int e = s_e[tid];
+        int p = 0, tiles = 0;
+        for (int q = 0; q < 8; ++q) {
+            const bool in = s_e[q] >= 0 && s_e[q] < 256;
+            p += in && (s_e[q] < e || (s_e[q] == e && q < tid));
+            bool first = in;
+            int c = 0;
+            for (int r = 0; r < 8; ++r) {
+                first = first && !(r < q && s_e[r] == s_e[q]);
+                c += s_e[r] == s_e[q];
+            }
+            if (first) tiles += (c + a.tile_rows - 1) / a.tile_rows;
+        }
+        if (e >= 0 && e < 256) {
+            a.pos[tid] = p;
+            a.perm[p] = tid;
+        } else {
+            a.pos[tid] = 0;
+        }
+        if (tid == 0) *a.num_tiles = tiles;
+    }
+    float* gu = reinterpret_cast<float*>(a.ws + a.L.dec) + kDecodeMaxT * 256;
+    for (int i = tid; i < (a.k + 1) * 2 * a.I; i += blockDim.x) gu[i] = 0.f;
+    float* acc = reinterpret_cast<float*>(a.ws + a.L.acc);
+    for (int i = tid; i < a.d; i += blockDim.x) acc[i] = 0.f;
+}
+}  // namespace
+
+cudaError_t launch_dispatch_prefill(const RouteArgs& a, cudaStream_t st, unsigned long long* launches) {
+    *launches += 3;
+    cudaError_t err = launch_with_pdl(route_count, dim3(a.L.nblk), dim3(256), 0, st, a);
+    if (err != cudaSuccess) return err;
+    if ((err = launch_with_pdl(route_scan, dim3(kScanCtas), dim3(1024), 0, st, a)) != cudaSuccess) return err;
+    return launch_with_pdl(route_scatter, dim3(a.L.nblk, a.k), dim3(256), 0, st, a);
+}
+
+cudaError_t launch_dispatch_decode(const RouteArgs& a, cudaStream_t st, unsigned long long* launches) {
+    *launches += 1;
+    return launch_with_pdl(dispatch_one, dim3(1), dim3(1024), 0, st, a);
+}
+
 cudaError_t launch_route_decode(const RouteArgs& a, cudaStream_t st, unsigned long long* launches) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];

@@ -1,0 +1,278 @@
+"""moe_gate and moe_dispatch on the GPU: against the definition in 64 bits (numpy), exact ties, switched-off
+experts, NaN and infinities, strides; the layer run through a gate equals the layer with its own router."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_grouped_gemm_gb300 as moe
+from gpu_helpers import DeviceLayer, to_dev
+from moe_workload import configs
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+F32_MAX = float(np.finfo(np.float32).max)
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+# fp32 scores: the argument of the exponential is off by at most 2^-24 (|l| + |m|) with |l| <= 32 here,
+# the exponential and the quotients by a few 2^-23, the sum of E terms by log2(E) 2^-24
+W_RTOL = 2.0 ** -23 * (32 + 16)
+# choice values nearer than this (relative to their scores) may be ranked either way; a sigmoid's argument is
+# exact, so only the exponential, a sum, a quotient and the bias' sum round: four times 2^-23
+GAP = {"softmax": 2 * W_RTOL, "sigmoid": 2 * 4 * 2.0 ** -23}
+
+
+def reference(l, bias, E, k, score, groups, group_topk, group_score, renormalise, scale):
+    """(idx, w, clear) in 64 bits; clear: no comparison that the choice rests on is within GAP, bar exact ties."""
+    T = l.shape[0]
+    l = l.astype(np.float64).copy()
+    l[np.isnan(l)] = -np.inf
+    l[l == np.inf] = F32_MAX
+    with np.errstate(over="ignore", invalid="ignore"):
+        if score == "sigmoid":
+            s = 1.0 / (1.0 + np.exp(-l))
+        else:
+            m = l.max(1, keepdims=True)
+            e = np.exp(l - np.where(np.isfinite(m), m, 0.0))
+            z = e.sum(1, keepdims=True)
+            s = e / np.where(z > 0, z, 1.0)
+    v = s if bias is None else s + bias.astype(np.float64)
+    size = s + (0.0 if bias is None else np.abs(bias.astype(np.float64)))
+    clear = np.ones(T, bool)
+
+    def sorted_clear(values, sizes, upto):
+        o = np.argsort(-values, 1, kind="stable")
+        sv, sz = np.take_along_axis(values, o, 1), np.take_along_axis(sizes, o, 1)
+        with np.errstate(invalid="ignore"):
+            gap = sv[:, :-1] - sv[:, 1:]
+        fine = (sv[:, :-1] == sv[:, 1:]) | (gap > GAP[score] * (sz[:, :-1] + sz[:, 1:]))
+        return o, fine[:, upto]
+
+    if groups > 1:
+        b = v.reshape(T, groups, E // groups)
+        best = -np.sort(-b, 2)
+        worth = best[:, :, 0] if group_score == "max" else best[:, :, 0] + best[:, :, 1]
+        gsize = np.broadcast_to(size.max(1, keepdims=True), worth.shape)
+        o, fine = sorted_clear(worth, gsize, slice(group_topk - 1, group_topk))
+        clear &= fine.all(1)
+        keep = np.zeros((T, groups), bool)
+        np.put_along_axis(keep, o[:, :group_topk], True, 1)
+        v = np.where(np.repeat(keep, E // groups, 1), v, -np.inf)
+        size = np.where(np.repeat(keep, E // groups, 1), size, 0.0)
+        # a kept expert at -inf (a NaN choice value) still precedes every dropped one
+        v = np.where(np.repeat(keep, E // groups, 1) & (v == -np.inf), -1e300, v)
+    o, fine = sorted_clear(v, size, slice(0, k))
+    clear &= fine.all(1)
+    idx = o[:, :k]
+    w = np.take_along_axis(s, idx, 1)
+    if renormalise:
+        z = w.sum(1, keepdims=True)
+        w = np.where(z > 0, w / np.where(z > 0, z, 1.0), 0.0)
+    return idx.astype(np.int32), w * scale, clear
+
+
+def run_gate(logits, bias, T, E, k, stride=0, **kw):
+    idx = torch.full((T + 1, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, k), -7.0, dtype=torch.float32, device="cuda")
+    cfg = moe.gate_config(T, E, k, dtype=logits.dtype, logits_stride=stride, **kw)
+    moe.moe_gate(cfg, logits, bias, idx, w)
+    torch.cuda.synchronize()
+    assert (idx[T:] == -7).all() and (w[T:] == -7).all(), "written past the last token"
+    return idx[:T].cpu().numpy(), w[:T].cpu().numpy()
+
+
+CASES = [
+    # T, E, k, dtype, score, groups, group_topk, group_score, bias, renormalise, scale, pad, switched off
+    (1, 256, 8, "f32", "sigmoid", 8, 4, "top2", True, True, 2.5, 0, 0.0),
+    (37, 256, 8, "f32", "softmax", 1, 1, "top2", False, True, 1.0, 0, 0.0),
+    (1000, 256, 8, "bf16", "sigmoid", 8, 3, "max", True, False, 1.0, 8, 0.1),
+    (129, 60, 6, "f16", "softmax", 1, 1, "top2", False, False, 1.0, 4, 0.2),
+    (65, 512, 10, "bf16", "softmax", 16, 4, "top2", True, True, 1.0, 0, 0.0),
+    (31, 1024, 32, "f32", "sigmoid", 32, 16, "max", False, True, 1.0, 1, 0.0),
+    (70, 1000, 17, "f16", "softmax", 4, 2, "top2", True, True, 0.5, 3, 0.3),
+    (9, 1, 1, "f32", "softmax", 1, 1, "top2", False, True, 1.0, 0, 0.0),
+    (9, 3, 3, "f32", "sigmoid", 1, 1, "top2", True, True, 1.0, 0, 0.5),
+    (40, 32, 32, "bf16", "softmax", 1, 1, "top2", False, True, 1.0, 0, 0.5),
+    (257, 33, 5, "f32", "softmax", 11, 3, "top2", True, False, 1.0, 0, 0.0),
+    (257, 96, 4, "f32", "sigmoid", 2, 1, "top2", True, True, 1.0, 0, 0.9),
+    (64, 300, 1, "bf16", "softmax", 1, 1, "top2", False, True, 1.0, 4, 0.0),
+    (64, 128, 2, "f16", "sigmoid", 4, 4, "top2", True, False, 1.0, 0, 0.0),
+]
+
+
+@pytest.mark.parametrize("T,E,k,dt,score,groups,gk,gs,with_bias,ren,scale,pad,off", CASES)
+def test_gate_against_64_bits(T, E, k, dt, score, groups, gk, gs, with_bias, ren, scale, pad, off):
+    g = torch.Generator().manual_seed(T * 1000 + E + k)
+    l = 2.0 * torch.randn(T, E, generator=g)
+    l[torch.rand(T, E, generator=g) < off] = -np.inf
+    if off:
+        l[:: 7] = -np.inf          # tokens with nothing left
+    buf = torch.full((T, E + pad), float("nan"), dtype=DT[dt])
+    buf[:, :E] = l.to(DT[dt])
+    bias = 0.3 * torch.randn(E, generator=g) if with_bias else None
+    idx, w = run_gate(buf.cuda(), None if bias is None else bias.cuda(), T, E, k, stride=E + pad, score=score,
+                      groups=groups, group_topk=gk, group_score=gs, renormalise=ren, scale=scale)
+    ri, rw, clear = reference(buf[:, :E].float().numpy(), None if bias is None else bias.numpy(), E, k, score, groups,
+                              gk, gs, ren, scale)
+    assert clear.mean() > 0.5 or T < 10
+    assert np.array_equal(idx[clear], ri[clear])
+    assert (np.abs(w - rw)[clear] <= W_RTOL * np.abs(rw)[clear] + 1e-30).all()
+    for t in range(T):
+        assert len(set(idx[t])) == k and idx[t].min() >= 0 and idx[t].max() < E
+
+
+def test_gate_ties_go_to_the_lower_index():
+    # four logit values only: nearly every comparison is an exact tie
+    g = torch.Generator().manual_seed(5)
+    for E, k, groups, gk in ((256, 8, 1, 1), (256, 8, 8, 4), (100, 20, 4, 2), (1024, 32, 1, 1)):
+        l = torch.randint(0, 4, (200, E), generator=g).float()
+        idx, w = run_gate(l.cuda(), None, 200, E, k, score="sigmoid", groups=groups, group_topk=gk)
+        ri, rw, clear = reference(l.numpy(), None, E, k, "sigmoid", groups, gk, "top2", True, 1.0)
+        assert clear.all() and np.array_equal(idx, ri)
+        assert (np.abs(w - rw) <= W_RTOL * rw).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_nan_and_infinities(score):
+    E, k = 64, 4
+    l = torch.linspace(-3, 3, E).repeat(7, 1)
+    l[0, 10] = float("nan")               # as if switched off
+    l[1, 10] = float("inf")               # first; the two of row 2 share
+    l[2, [5, 50]] = float("inf")
+    l[3] = float("nan")
+    l[4] = -float("inf")
+    l[5] = -float("inf")
+    l[5, 33] = 1.0                        # one expert left
+    l[6] = -3.0e38
+    ri, rw, _ = reference(l.numpy(), None, E, k, score, 1, 1, "top2", True, 1.0)
+    for t in (torch.float32, torch.bfloat16):
+        idx, w = run_gate(l.to(t).cuda(), None, 7, E, k, score=score)
+        assert idx[1][0] == 10 and set(idx[2][:2]) == {5, 50}
+        assert list(idx[3]) == [0, 1, 2, 3] == list(idx[4]) and (w[3:5] == 0).all()
+        assert idx[5][0] == 33 and list(idx[5][1:]) == [0, 1, 2] and list(w[5]) == [1, 0, 0, 0]
+        assert np.isfinite(w).all()
+        if t == torch.float32:
+            assert np.array_equal(idx[[0, 1, 2, 3, 4, 5]], ri[[0, 1, 2, 3, 4, 5]])
+            assert np.abs(w[:6] - rw[:6]).max() <= W_RTOL
+            if score == "softmax":
+                assert np.abs(w[6] - 0.25).max() <= W_RTOL
+
+
+def test_gate_nan_in_the_bias_switches_the_expert_off():
+    l = torch.randn(50, 40, generator=torch.Generator().manual_seed(1))
+    b = torch.zeros(40)
+    b[7] = float("nan")
+    idx, w = run_gate(l.cuda(), b.cuda(), 50, 40, 6, score="sigmoid")
+    assert not (idx == 7).any() and np.isfinite(w).all()
+
+
+def test_gate_unaligned_logits_and_zero_tokens():
+    l = torch.randn(20, 257, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    view = l[:, 1:]                       # rows at odd elements
+    a = run_gate(view, None, 20, 256, 8, stride=257)
+    b = run_gate(view.contiguous(), None, 20, 256, 8)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+    run_gate(l, None, 0, 256, 8)
+
+
+def test_gate_on_another_stream():
+    s = torch.cuda.Stream()
+    l = torch.randn(3000, 256, device="cuda")
+    idx = torch.empty(3000, 8, dtype=torch.int32, device="cuda")
+    w = torch.empty(3000, 8, device="cuda")
+    cfg = moe.gate_config(3000)
+    s.wait_stream(torch.cuda.current_stream())
+    moe.moe_gate(cfg, l, None, idx, w, stream=s)
+    s.synchronize()
+    i2, w2 = run_gate(l, None, 3000, 256, 8)
+    assert np.array_equal(idx.cpu().numpy(), i2) and np.array_equal(w.cpu().numpy(), w2)
+
+
+def test_gate_refusal_raises():
+    l = torch.zeros(4, 256, device="cuda")
+    i = torch.zeros(4, 8, dtype=torch.int32, device="cuda")
+    with pytest.raises(moe.MoEError):
+        moe.moe_gate(moe.gate_config(4, 256, 8, groups=5, group_topk=2), l, None, i, l)
+
+
+# ------------------------------------------------------------------------------- moe_dispatch
+
+
+def layer(T, d=512, I=128):
+    wl = configs.custom_workload(f"gate_t{T}", T=T, d=d, I=I)
+    shp = moe.shape(T, d, 256, 8, I, I)
+    return shp, DeviceLayer(shp, configs.make_layer(wl)), configs.make_x(wl)
+
+
+@pytest.mark.parametrize("T", [1, 2, 33, 500])
+def test_layer_through_the_gate_equals_the_layer_with_its_router(T):
+    shp, dl, x = layer(T)
+    xd = to_dev(x)
+    opts = moe.options(deterministic=1, decode_path=moe.DECODE_GEMV)
+    outs, rts = [], []
+    for own_router in (True, False):
+        rt, ws = moe.Routing(T), moe.workspace(shp, opts)
+        y = torch.empty(T, shp.d, dtype=torch.int16, device="cuda")
+        for _ in range(2):                 # the second call finds the first one's workspace
+            if own_router:
+                moe.moe_route(shp, xd, dl.w_router, None, rt, ws, opts)
+            else:
+                lg = torch.empty(T, 256, device="cuda")
+                moe.moe_router_logits(shp, xd, dl.w_router, None, lg)
+                moe.moe_gate(moe.gate_config(T), lg, None, rt.topk_idx, rt.topk_w)
+                rt.topk_w.copy_(rts[0].topk_w)   # the same weights to the last bit
+                moe.moe_dispatch(shp, xd, rt, ws, opts)
+            moe.moe_grouped_ffn(shp, xd, rt, dl.packed_routed, dl.packed_shared, ws, opts)
+            moe.moe_combine(shp, rt, ws, y, opts)
+            rc, bits = moe.moe_read_status(ws)
+            assert rc == moe.MOE_OK, bits
+        outs.append(y.clone())
+        rts.append(rt)
+    a, b = rts
+    n = int(a.num_tiles.item())
+    assert n == int(b.num_tiles.item())
+    for f in ("topk_idx", "counts", "offsets", "perm", "pos"):
+        assert torch.equal(getattr(a, f), getattr(b, f)), f
+    assert torch.equal(a.tiles[:n], b.tiles[:n])
+    if T > 1:
+        assert torch.equal(outs[0], outs[1])
+    else:   # the decode kernels add partial rows with atomics: their order is not fixed
+        f = [o.view(torch.bfloat16).float() for o in outs]
+        assert (f[0] - f[1]).abs().max() <= 2.0 ** -7 * f[0].abs().max()
+
+
+def test_dispatch_of_a_skewed_choice():
+    """Every token picks expert 255 and seven more; counts, offsets, perm and pos from their definition."""
+    T = 333
+    shp, dl, x = layer(T)
+    rng = np.random.RandomState(0)
+    idx = np.stack([np.concatenate([[255], rng.permutation(255)[:7]]) for _ in range(T)]).astype(np.int32)
+    rt, ws = moe.Routing(T), moe.workspace(shp)
+    rt.topk_idx.copy_(torch.from_numpy(idx))
+    rt.topk_w.fill_(0.125)
+    moe.moe_dispatch(shp, to_dev(x), rt, ws)
+    assert moe.moe_read_status(ws)[0] == moe.MOE_OK
+    flat = idx.reshape(-1)
+    counts = np.bincount(flat, minlength=256)
+    order = np.argsort(flat, kind="stable")
+    assert np.array_equal(rt.counts.cpu().numpy(), counts)
+    assert np.array_equal(rt.offsets.cpu().numpy(), np.concatenate([[0], np.cumsum(counts)]))
+    assert np.array_equal(rt.perm.cpu().numpy(), order)
+    pos = np.empty(8 * T, np.int64)
+    pos[order] = np.arange(8 * T)
+    assert np.array_equal(rt.pos.cpu().numpy().reshape(-1), pos)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_dispatch_flags_an_expert_out_of_range(T):
+    shp, dl, x = layer(T)
+    rt, ws = moe.Routing(T), moe.workspace(shp)
+    rt.topk_idx.copy_(torch.arange(8, dtype=torch.int32).repeat(T, 1))
+    rt.topk_idx[T - 1, 3] = 256
+    rt.topk_idx[0, 5] = -1
+    rt.topk_w.fill_(0.125)
+    moe.moe_dispatch(shp, to_dev(x), rt, ws)
+    rc, bits = moe.moe_read_status(ws)
+    assert rc == moe.MOE_ERR_DEVICE_STATUS and bits & moe.MOE_STATUS_BAD_EXPERT
+    assert int(rt.counts.sum()) == 8 * T - 2
+    pos = rt.pos.cpu().numpy()
+    assert pos.min() >= 0 and pos.max() < 8 * T
