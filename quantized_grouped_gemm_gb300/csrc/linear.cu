@@ -127,15 +127,58 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t linear_workspace(const LinearArgs& a) {
-    (void)a;
-    return 256;
+// Operands whose rows do not start at multiples of 16 bytes are copied to rows that do, for the tensor-core
+// kernels (TMA reads rows at such addresses only).
+constexpr int kFewTokens = 32;   // at most this many: linear_rows
+
+static bool straight(long long stride) { return stride % 8 == 0; }
+static long long padded(int K) { return (K + 7) / 8 * 8; }
+
+__global__ void __launch_bounds__(256) realign_rows(const uint16_t* __restrict__ src, long long src_stride, int K,
+                                                    uint16_t* __restrict__ dst, long long dst_stride) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const uint16_t* s = src + (long long)blockIdx.x * src_stride;
+    uint4* d = reinterpret_cast<uint4*>(dst + (long long)blockIdx.x * dst_stride);
+    for (int c = threadIdx.x; c < (int)(dst_stride / 8); c += blockDim.x) d[c] = load8<false>(s + 8 * c, K - 8 * c);
 }
 
-cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st, unsigned long long* launches) {
+size_t linear_workspace(const LinearArgs& a) {
+    size_t n = 256;
+    if (a.T > kFewTokens) {
+        if (!straight(a.w_stride)) n += align_up((size_t)a.rows * padded(a.K) * 2, 256);
+        if (!straight(a.x_stride)) n += align_up((size_t)a.T * padded(a.K) * 2, 256);
+    }
+    return n;
+}
+
+cudaError_t launch_linear(const LinearArgs& args, cudaStream_t st, unsigned long long* launches) {
+    LinearArgs a = args;
     *launches += 1;
-    if (a.f16) return a.out_f32 ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);
-    return a.out_f32 ? launch_rows<false, true>(a, st) : launch_rows<false, false>(a, st);
+    if (a.T <= kFewTokens) {
+        if (a.f16) return a.out_f32 ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);
+        return a.out_f32 ? launch_rows<false, true>(a, st) : launch_rows<false, false>(a, st);
+    }
+    uint8_t* at = a.ws + 256;
+    const long long stride = padded(a.K);
+    if (!straight(a.w_stride)) {
+        const cudaError_t e = launch_with_pdl(realign_rows, dim3(a.rows), dim3(256), 0, st, static_cast<const uint16_t*>(a.w),
+                                              a.w_stride, a.K, reinterpret_cast<uint16_t*>(at), stride);
+        if (e != cudaSuccess) return e;
+        a.w = at;
+        a.w_stride = stride;
+        at += align_up((size_t)a.rows * stride * 2, 256);
+        *launches += 1;
+    }
+    if (!straight(a.x_stride)) {
+        const cudaError_t e = launch_with_pdl(realign_rows, dim3(a.T), dim3(256), 0, st, static_cast<const uint16_t*>(a.x),
+                                              a.x_stride, a.K, reinterpret_cast<uint16_t*>(at), stride);
+        if (e != cudaSuccess) return e;
+        a.x = at;
+        a.x_stride = stride;
+        *launches += 1;
+    }
+    return launch_linear_tc(a, st);
 }
 
 }  // namespace moe

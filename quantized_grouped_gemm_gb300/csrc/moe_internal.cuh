@@ -771,11 +771,14 @@ struct LinearArgs {
     int num_sms;
 };
 size_t linear_workspace(const LinearArgs& a);
+cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t st);   // linear_tc.cu; rows at multiples of 16 bytes
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st, unsigned long long* launches);
 
 // Encodes 2-D bf16 tensor maps (host; driver entry point fetched through the runtime).
 cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                               uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
                               bool swizzle128 = true);
+cudaError_t make_tmap_f32_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                             uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows);
 
 }  // namespace moe
