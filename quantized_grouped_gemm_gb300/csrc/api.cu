@@ -447,7 +447,8 @@ int moe_gate(const moe_gate_config* c, const void* logits, const float* bias, in
         return MOE_ERR_INVALID_ARG;
     GateArgs a{};
     a.T = c->T; a.E = c->E; a.k = c->k;
-    a.groups = groups; a.group_topk = c->group_topk;
+    a.groups = groups; a.group_topk = c->group_topk; a.per = c->E / groups;
+    a.f16 = c->logits_type == MOE_F16;
     a.sigmoid = c->score == MOE_SCORE_SIGMOID;
     a.group_max = c->group_score == MOE_GROUP_MAX;
     a.renormalise = c->renormalise == 1;

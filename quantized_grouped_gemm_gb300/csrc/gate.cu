@@ -1,205 +1,396 @@
 // gate.cu -- the gate over given router logits (moe_gate): scores, groups, top-k, weights.
 //
-// One warp per token.  Lane l holds the P = 2^p >= E/32 consecutive experts l*P .. l*P + P-1, so the
-// order (lane, position) is the order of the expert indices and ties resolve to the lower index by
-// taking the lowest lane.
+// One warp per token, no memory traffic but the logits in and the choice out.  The lanes are shared out
+// among the groups (all 32 to the one group where there are none); a lane holds up to P consecutive
+// experts of its group, so the order (lane, position) is the order of the expert indices.
+//
+// The kernel is bound by instructions, not by its bytes (256 fp32 logits are 32 a lane), so the top k are
+// found without sorting E values.  Each lane takes the maximum of each of S parts of its values; the k-th
+// largest of these 32 S samples is a lower bound B of the k-th largest value (k samples are >= B), so only
+// values >= B can be chosen -- about 9 of 256 for k = 8.  Those are compacted through shared memory, and each
+// finds its rank by counting the ones above it.  Ties (found by the ranks not being a permutation) and
+// tokens with more than kMaxCand candidates (ties by the hundred, as when every expert is switched off) take
+// k rounds of a warp-wide argmax instead.
 #include "moe_internal.cuh"
 
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <math_constants.h>
 
 namespace moe {
 namespace {
 
 constexpr int kGateWarps = 8;
+constexpr int kMaxCand = 128;   // candidates ranked by counting: up to 4 a lane
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kInf = __builtin_huge_valf(), kMaxF = 3.402823466e+38f;
 
-__device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+// How the choice values come about.
+enum GateMode {
+    kLogits,        // neither bias nor groups: scores rise with the logits, which are compared themselves (those
+                    // whose score is 0 as equals); only the chosen experts' scores are computed
+    kLogitsTotal,   // the same, with the softmax's sum over all experts (weights not renormalised)
+    kScores,        // a bias: every expert's score
+    kGroups         // groups, with or without a bias
+};
 
-// Order-preserving key of a choice value (+0 and -0 alike); -inf maps to 0x007fffff, so 0 stays free
-// for "cannot be chosen".  NaN counts as -inf.
-__device__ __forceinline__ uint32_t choice_key(float v) {
-    if (!(v == v)) v = -CUDART_INF_F;
-    v += 0.0f;
-    const uint32_t u = __float_as_uint(v);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+__device__ __forceinline__ float warp_max(float v) {   // a NaN operand is dropped
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
 }
 
-template <typename T> __device__ __forceinline__ float to_f32(T v);
-template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+// exp(x) = 2^t 2^r with t = x log2(e) rounded and r what the rounding left; the hardware's 2^t is good to
+// about 2^-22, and 2^r = 1 + r ln 2 to first order (|r| < 2^-16 for |x| < 100).
+__device__ __forceinline__ float exp_f32(float x) {
+    const float t = x * 1.44269504f;
+    const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504f, -t));   // log2(e) = 1.44269504 + 1.926e-8 as floats
+    float p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+    return fmaf(p * 0.693147181f, r, p);
+}
+// Scores; those below exp(kLowest), next to the smallest normal number, are 0, and so are those of -inf and NaN.
+constexpr float kLowest = -87.0f;
+__device__ __forceinline__ float sigmoid_score(float l) {
+    const float d = 1.0f + exp_f32(fminf(fmaxf(-l, -88.0f), -kLowest));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return l > kLowest ? r : 0.0f;
+}
+__device__ __forceinline__ float softmax_term(float x) { return x > kLowest ? exp_f32(x) : 0.0f; }   // x = logit - largest
 
-template <typename T, int P, bool kSigmoid, bool kGroups>
+template <typename T> __device__ __forceinline__ float logit_f32(T v, bool f16);
+template <> __device__ __forceinline__ float logit_f32<float>(float v, bool) { return v; }
+template <> __device__ __forceinline__ float logit_f32<uint16_t>(uint16_t v, bool f16) {
+    return f16 ? __half2float(__ushort_as_half(v)) : bf16f(v);
+}
+
+// P: the most experts a lane holds (fewer at the end of a group); S: samples a lane gives to the bound.
+template <typename T, int P, int S, GateMode kMode>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
+    constexpr bool kByScore = kMode == kScores || kMode == kGroups;
+    __shared__ __align__(16) float c_v[kGateWarps][kMaxCand];   // the candidates' values,
+    __shared__ float2 c_se[kGateWarps][kMaxCand];               // scores and indices
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long tok = (long long)blockIdx.x * kGateWarps + warp;
-    __shared__ float s_group[kGateWarps][32];
     pdl_wait();
     pdl_launch_dependents();
     if (tok >= a.T) return;
-    const int E = a.E, e0 = lane * P;
-    const T* row = static_cast<const T*>(a.logits) + tok * a.stride;
+    // this lane's experts: e0 .. e0 + cnt - 1
+    const int lpg = 1 << a.lane_shift, g = lane >> a.lane_shift, sub = lane & (lpg - 1);
+    const int e0 = g * a.per + sub * P;
+    const int cnt = a.full ? P : g < a.groups ? max(0, min(P, a.per - sub * P)) : 0;
+    const T* row = static_cast<const T*>(a.logits) + tok * a.stride + e0;
 
-    float s[P];   // logits, then scores
-#pragma unroll
-    for (int i = 0; i < P; ++i) s[i] = -CUDART_INF_F;
+    float s[P];   // logits (softmax: minus the largest), then with kByScore scores
     constexpr int V = 16 / (int)sizeof(T) < P ? 16 / (int)sizeof(T) : P;   // elements of a vector load
-    if (a.vec && V * sizeof(T) == 16) {
+    if (V * sizeof(T) == 16 && a.vec) {
 #pragma unroll
         for (int c = 0; c < P; c += V) {
-            if (e0 + c + V <= E) {
-                const uint4 q = ld_nc_v4(row + e0 + c);
-                const T* t = reinterpret_cast<const T*>(&q);
+            if (a.full || c + V <= cnt) {
+                const uint4 q = ld_nc_v4(row + c);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[c + i] = to_f32(t[i]);
+                for (int i = 0; i < V; ++i) {
+                    if (sizeof(T) == 4) s[c + i] = __uint_as_float(w[i % 4]);
+                    else s[c + i] = logit_f32<uint16_t>((uint16_t)(w[(i / 2) % 4] >> (16 * (i % 2))), a.f16);
+                }
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (e0 + c + i < E) s[c + i] = to_f32(row[e0 + c + i]);
+                for (int i = 0; i < V; ++i) s[c + i] = c + i < cnt ? logit_f32<T>(row[c + i], a.f16) : -kInf;
             }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (e0 + i < E) s[i] = to_f32(row[e0 + i]);
+        for (int i = 0; i < P; ++i) s[i] = i < cnt ? logit_f32<T>(row[i], a.f16) : -kInf;
     }
-    // NaN counts as -inf, +inf as the largest finite number (fmaxf drops a NaN operand)
-#pragma unroll
-    for (int i = 0; i < P; ++i) s[i] = fminf(fmaxf(s[i], -CUDART_INF_F), CUDART_MAX_NORMAL_F);
 
-    if (kSigmoid) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) s[i] = __fdividef(1.0f, 1.0f + expf(-s[i]));   // exp(inf): 1 / inf = 0
-    } else {
+    float inv = 1.0f;
+    if (!a.sigmoid) {
         float m = s[0];
 #pragma unroll
-        for (int i = 1; i < P; ++i) m = fmaxf(m, s[i]);
+        for (int i = 1; i < P; ++i) m = fmaxf(m, s[i]);   // fmaxf drops a NaN
+        m = warp_max(m);
+        if (!(fabsf(m) <= kMaxF)) {   // +inf counts as the largest number; nothing left: every score is 0
+            m = m > 0.0f ? kMaxF : 0.0f;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (m == -CUDART_INF_F) m = 0.0f;   // nothing left: every score is exp(-inf) = 0
-        float z = 0.0f;
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            s[i] = expf(s[i] - m);
-            z += s[i];
+            for (int i = 0; i < P; ++i) s[i] = fminf(fmaxf(s[i], -kInf), kMaxF);
         }
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        const float r = z > 0.0f ? 1.0f / z : 0.0f;
-#pragma unroll
-        for (int i = 0; i < P; ++i) s[i] *= r;
-    }
-
-    // choice values as keys; experts beyond E cannot be chosen
-    uint32_t key[P];
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const float v = a.bias && e0 + i < E ? s[i] + __ldg(a.bias + e0 + i) : s[i];
-        key[i] = e0 + i < E ? choice_key(v) : 0u;
-    }
-
-    if (kGroups) {
-        // worth of group g, then the groups kept: a bit per group
-        const int per = E / a.groups;
-        for (int g = 0; g < a.groups; ++g) {
-            uint32_t k1 = 0, k2 = 0;   // this lane's two best of the group
+        for (int i = 0; i < P; ++i) s[i] -= m;
+        if (kMode != kLogits) {
+            float z = 0.0f;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const int e = e0 + i;
-                if (e >= g * per && e < (g + 1) * per) {
-                    k2 = max(k2, min(k1, key[i]));
-                    k1 = max(k1, key[i]);
-                }
+                const float x = softmax_term(s[i]);
+                z += x;
+                if (kByScore) s[i] = x;
             }
-            const uint32_t b1 = warp_max_u32(k1);
-            const uint32_t has = __ballot_sync(0xffffffffu, k1 == b1);
-            const uint32_t b2 = warp_max_u32(lane == __ffs(has) - 1 ? k2 : k1);
-            const auto val = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k); };
-            if (lane == g) s_group[warp][g] = a.group_max ? val(b1) : val(b1) + val(b2);
-        }
-        __syncwarp();
-        uint32_t mine = lane < a.groups ? choice_key(s_group[warp][lane]) : 0u;
-        int rank = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const uint32_t other = choice_key(s_group[warp][g]);
-            rank += other > mine || (other == mine && g < lane);
-        }
-        const uint32_t kept = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.group_topk);
+            z = warp_sum(z);
+            inv = z > 0.0f ? 1.0f / z : 0.0f;
+            if (kByScore) {
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (e0 + i < E && !((kept >> ((e0 + i) / per)) & 1u)) key[i] = 0u;
+                for (int i = 0; i < P; ++i) s[i] *= inv;
+            }
+        }
+    } else if (kByScore) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) s[i] = sigmoid_score(s[i]);
     }
 
-    // k rounds: the warp's largest key, the lowest lane that has it, that lane's first position
-    int my_e = 0;
-    float my_s = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t best = key[0];
+    // choice values (at least -FLT_MAX, also for NaN); -inf marks what cannot be chosen
+    float v[P];
+    if (kByScore) {
+        if (a.bias) {
+            if (P % 4 == 0 && a.bias_vec) {
 #pragma unroll
-        for (int i = 1; i < P; ++i) best = max(best, key[i]);
-        const uint32_t top = warp_max_u32(best);
-        const int from = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-        int e = 0;
-        float sc = 0.0f;
-        if (lane == from) {
-            bool found = false;
+                for (int c = 0; c < P; c += 4) {
+                    if (a.full || c + 4 <= cnt) {
+                        const float4 b = ld_nc_f4(a.bias + e0 + c);
+                        v[c] = s[c] + b.x; v[(c + 1) % P] = s[(c + 1) % P] + b.y;
+                        v[(c + 2) % P] = s[(c + 2) % P] + b.z; v[(c + 3) % P] = s[(c + 3) % P] + b.w;
+                    } else {
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (!found && key[i] == top) {
-                    found = true;
-                    key[i] = 0u;
-                    e = e0 + i;
-                    sc = s[i];
+                        for (int i = c; i < c + 4 && i < P; ++i) v[i] = i < cnt ? s[i] + __ldg(a.bias + e0 + i) : 0.0f;
+                    }
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) v[i] = i < cnt ? s[i] + __ldg(a.bias + e0 + i) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = fmaxf(v[i], -kMaxF);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = s[i];
         }
-        e = __shfl_sync(0xffffffffu, e, from);
-        sc = __shfl_sync(0xffffffffu, sc, from);
-        if (lane == j) {
-            my_e = e;
-            my_s = sc;
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = s[i] = fminf(fmaxf(s[i], kLowest), kMaxF);
+    }
+    if (!a.full) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (i >= cnt) v[i] = -kInf;
+    }
+
+    if (kMode == kGroups && a.group_topk < a.groups) {
+        // the two best of the lane, then of the group's lanes
+        float v1 = v[0], v2 = -kInf;
+#pragma unroll
+        for (int i = 1; i < P; ++i) {
+            v2 = fmaxf(v2, fminf(v1, v[i]));
+            v1 = fmaxf(v1, v[i]);
+        }
+        for (int o = lpg >> 1; o >= 1; o >>= 1) {
+            const float o1 = __shfl_xor_sync(kAll, v1, o), o2 = __shfl_xor_sync(kAll, v2, o);
+            v2 = fmaxf(fmaxf(v2, o2), fminf(v1, o1));
+            v1 = fmaxf(v1, o1);
+        }
+        // the group_topk best groups, one a round, the lowest lane (so the lowest group) first
+        float worth = g < a.groups ? fmaxf(a.group_max ? v1 : v1 + v2, -kMaxF) : -kInf;
+        bool kept = false;
+        for (int j = 0; j < a.group_topk; ++j) {
+            const float top = warp_max(worth);
+            const int who = (__ffs(__ballot_sync(kAll, worth == top)) - 1) >> a.lane_shift;
+            if (g == who) {
+                kept = true;
+                worth = -kInf;
+            }
+        }
+        if (!kept) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = -kInf;
         }
     }
-    float w = lane < a.k ? my_s : 0.0f;
-    if (a.renormalise) {
-        float z = w;
+
+    // candidates: one a lane where a lane holds one expert anyway
+    float cv = v[0], cs = s[0];
+    int ce = e0, cand = 32;
+    if (P > 1) {
+        float h[S];
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        for (int q = 0; q < S; ++q) {
+            h[q] = v[q * (P / S)];
+#pragma unroll
+            for (int i = 1; i < P / S; ++i) h[q] = fmaxf(h[q], v[q * (P / S) + i]);
+        }
+        float bound = -kMaxF;
+#pragma unroll 4
+        for (int j = 0; j < a.k; ++j) {   // equal samples leave together, which only lowers the bound
+            float best = h[0];
+#pragma unroll
+            for (int q = 1; q < S; ++q) best = fmaxf(best, h[q]);
+            const float top = warp_max(best);
+            bound = top;
+#pragma unroll
+            for (int q = 0; q < S; ++q)
+                if (h[q] == top) h[q] = -kInf;
+        }
+        bound = fmaxf(bound, -kMaxF);     // fewer than k samples: everything that can be chosen
+        const uint32_t below = (1u << lane) - 1u;
+        c_v[warp][lane] = -kInf;          // ranks are counted in fours
+        __syncwarp();
+        cand = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const bool in = v[i] >= bound;
+            const uint32_t mask = __ballot_sync(kAll, in);
+            const int at = cand + __popc(mask & below);
+            cand += __popc(mask);
+            if (in && at < kMaxCand) {
+                c_v[warp][at] = v[i];
+                c_se[warp][at] = make_float2(s[i], __int_as_float(e0 + i));
+            }
+        }
+        __syncwarp();
+        if (cand <= 32) {
+            cv = c_v[warp][lane];
+            const float2 se = c_se[warp][lane & (cand > lane ? 31 : 0)];
+            cs = se.x;
+            ce = __float_as_int(se.y);
+        }
+    }
+
+    int slot = -1;   // the chosen expert of this lane, if any: slot, index, score (or logit)
+    bool done = false;
+    if (P > 1 && cand <= 32) {
+        int rank = 0;
+        for (int j = 0; j < cand; j += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(&c_v[warp][j]);
+            rank += (o.x > cv) + (o.y > cv) + (o.z > cv) + (o.w > cv);
+        }
+        // no ties: the ranks of the candidates are 0 .. cand - 1
+        done = __reduce_or_sync(kAll, lane < cand ? 1u << rank : 0u) == kAll >> (32 - cand);
+        if (done && lane < cand && rank < a.k) slot = rank;
+    }
+    if (!done && cand <= 32) {
+        for (int j = 0; j < a.k; ++j) {
+            const float top = warp_max(cv);
+            const uint32_t low = __reduce_min_sync(kAll, cv == top ? (uint32_t)ce : kAll);
+            if (cv == top && (uint32_t)ce == low) {
+                slot = j;
+                cv = -kInf;
+            }
+        }
+    } else if (!done && cand <= kMaxCand) {
+        float qv[kMaxCand / 32];
+#pragma unroll
+        for (int q = 0; q < kMaxCand / 32; ++q) qv[q] = lane + 32 * q < cand ? c_v[warp][lane + 32 * q] : -kInf;
+        for (int j = 0; j < a.k; ++j) {
+            float best = qv[0];
+#pragma unroll
+            for (int q = 1; q < kMaxCand / 32; ++q) best = fmaxf(best, qv[q]);
+            const float top = warp_max(best);
+            uint32_t low = kAll;   // lowest index among the equals, with its place in the buffer
+#pragma unroll
+            for (int q = 0; q < kMaxCand / 32; ++q)
+                if (qv[q] == top)
+                    low = min(low, ((uint32_t)__float_as_int(c_se[warp][lane + 32 * q].y) << 8) | (uint32_t)(lane + 32 * q));
+            low = __reduce_min_sync(kAll, low);
+            const int at = low & 0xff;
+#pragma unroll
+            for (int q = 0; q < kMaxCand / 32; ++q)
+                if (at == lane + 32 * q) qv[q] = -kInf;
+            if (lane == j) {
+                slot = j;
+                ce = low >> 8;
+                cs = c_se[warp][at].x;
+            }
+        }
+    } else if (!done) {
+        for (int j = 0; j < a.k; ++j) {
+            float best = v[0];
+#pragma unroll
+            for (int i = 1; i < P; ++i) best = fmaxf(best, v[i]);
+            const float top = warp_max(best);
+            const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
+            int e = 0;
+            float sc = 0.0f;
+            if (lane == from) {
+                bool found = false;
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    if (!found && v[i] == top) {
+                        found = true;
+                        v[i] = -kInf;
+                        e = e0 + i;
+                        sc = s[i];
+                    }
+            }
+            e = __shfl_sync(kAll, e, from);
+            sc = __shfl_sync(kAll, sc, from);
+            if (lane == j) {
+                slot = j;
+                ce = e;
+                cs = sc;
+            }
+        }
+    }
+
+    float w = cs;
+    if (!kByScore) w = a.sigmoid ? sigmoid_score(cs) : softmax_term(cs) * inv;
+    if (slot < 0) w = 0.0f;
+    if (a.renormalise) {
+        const float z = warp_sum(w);
         w = z > 0.0f ? w / z : 0.0f;
     }
-    if (lane < a.k) {
-        a.topk_idx[tok * a.k + lane] = my_e;
-        a.topk_w[tok * a.k + lane] = w * a.scale;
+    if (slot >= 0) {
+        a.topk_idx[tok * a.k + slot] = ce;
+        a.topk_w[tok * a.k + slot] = w * a.scale;
     }
 }
 
-template <typename T, int P>
-cudaError_t launch_p(const GateArgs& a, cudaStream_t st) {
+template <typename T, int P, int S>
+cudaError_t launch_ps(const GateArgs& a, cudaStream_t st) {
     const dim3 grid((unsigned)((a.T + kGateWarps - 1) / kGateWarps)), block(32 * kGateWarps);
-    if (a.sigmoid)
-        return a.groups > 1 ? launch_with_pdl(gate_kernel<T, P, true, true>, grid, block, 0, st, a)
-                            : launch_with_pdl(gate_kernel<T, P, true, false>, grid, block, 0, st, a);
-    return a.groups > 1 ? launch_with_pdl(gate_kernel<T, P, false, true>, grid, block, 0, st, a)
-                        : launch_with_pdl(gate_kernel<T, P, false, false>, grid, block, 0, st, a);
+    if (a.groups > 1) return launch_with_pdl(gate_kernel<T, P, S, kGroups>, grid, block, 0, st, a);
+    if constexpr (P <= 32) {   // a lane holds more than 32 experts only where groups leave lanes idle
+        if (a.bias) return launch_with_pdl(gate_kernel<T, P, S, kScores>, grid, block, 0, st, a);
+        if (!a.sigmoid && !a.renormalise) return launch_with_pdl(gate_kernel<T, P, S, kLogitsTotal>, grid, block, 0, st, a);
+        return launch_with_pdl(gate_kernel<T, P, S, kLogits>, grid, block, 0, st, a);
+    }
+    return cudaErrorInvalidValue;
+}
+
+// Samples: one a lane while k is at most two fifths of the lanes that can hold a chosen expert (about 1.3 k
+// candidates then), else four.
+template <typename T, int P>
+cudaError_t launch_p(GateArgs a, cudaStream_t st) {
+    a.full = a.per == P << a.lane_shift && a.groups << a.lane_shift == 32;
+    if constexpr (P >= 8) {
+        const int lanes = a.groups > 1 ? a.group_topk << a.lane_shift : 32;
+        if (5 * a.k > 2 * lanes) return launch_ps<T, P, 4>(a, st);
+    }
+    return launch_ps<T, P, 1>(a, st);
 }
 
 template <typename T>
-cudaError_t launch_t(const GateArgs& a, cudaStream_t st) {
-    if (a.E <= 32) return launch_p<T, 1>(a, st);
-    if (a.E <= 64) return launch_p<T, 2>(a, st);
-    if (a.E <= 128) return launch_p<T, 4>(a, st);
-    if (a.E <= 256) return launch_p<T, 8>(a, st);
-    if (a.E <= 512) return launch_p<T, 16>(a, st);
-    return launch_p<T, 32>(a, st);
+cudaError_t launch_t(GateArgs a, cudaStream_t st) {
+    int lanes = 32;   // of a group: a power of two
+    while (lanes * a.groups > 32) lanes /= 2;
+    a.lane_shift = lanes == 32 ? 5 : lanes == 16 ? 4 : lanes == 8 ? 3 : lanes == 4 ? 2 : lanes == 2 ? 1 : 0;
+    const int need = (a.per + lanes - 1) / lanes;
+    // vector loads: every group and lane starts at a multiple of 16 bytes
+    a.vec = a.vec && (a.groups == 1 || a.per * sizeof(T) % 16 == 0);
+    a.bias_vec = reinterpret_cast<uintptr_t>(a.bias) % 16 == 0 && (a.groups == 1 || a.per % 4 == 0);
+    if (need <= 1) return launch_p<T, 1>(a, st);
+    if (need <= 2) return launch_p<T, 2>(a, st);
+    if (need <= 4) return launch_p<T, 4>(a, st);
+    if (need <= 8) return launch_p<T, 8>(a, st);
+    if (need <= 16) return launch_p<T, 16>(a, st);
+    if (need <= 32) return launch_p<T, 32>(a, st);
+    return launch_p<T, 64>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_gate(const GateArgs& a, int logits_type, cudaStream_t st, unsigned long long* launches) {
     *launches += 1;
-    if (logits_type == MOE_BF16) return launch_t<__nv_bfloat16>(a, st);
-    if (logits_type == MOE_F16) return launch_t<__half>(a, st);
-    return launch_t<float>(a, st);
+    return logits_type == MOE_F32 ? launch_t<float>(a, st) : launch_t<uint16_t>(a, st);
 }
 
 }  // namespace moe

@@ -741,8 +741,10 @@ cudaError_t launch_scale_check(size_t n, const uint16_t* scales, int* mode, cuda
 struct GateArgs {
     int T, E, k;
     int groups, group_topk;
-    bool sigmoid, group_max, renormalise;
-    bool vec;                  // logits rows start at multiples of 16 bytes
+    int per, lane_shift;       // experts of a group, log2 of its lanes (set at launch)
+    bool sigmoid, group_max, renormalise, f16;
+    bool vec, bias_vec;        // logits rows (bias) start at multiples of 16 bytes
+    bool full;                 // every lane holds as many experts as it may (set at launch)
     float scale;
     const void* logits;
     long long stride;
