@@ -65,13 +65,12 @@ def options(tile_rows: int = 32, decode_max_tokens: int = 1, decode_path: int = 
 
 
 def _p(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _s(stream: Optional[torch.cuda.Stream]):
     # the raw handle of the current stream: a Stream object costs about 3 us a call, as much as a launch
-    s = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
-    return ctypes.c_void_p(s)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _o(opts):

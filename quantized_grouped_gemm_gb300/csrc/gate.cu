@@ -43,15 +43,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// exp(x) = 2^t 2^r with t = x log2(e) rounded and r what the rounding left; the hardware's 2^t is good to
-// about 2^-22, and 2^r = 1 + r ln 2 to first order (|r| < 2^-16 for |x| < 100).
-__device__ __forceinline__ float exp_f32(float x) {
-    const float t = x * 1.44269504f;
-    const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504f, -t));   // log2(e) = 1.44269504 + 1.926e-8 as floats
-    float p;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
-    return fmaf(p * 0.693147181f, r, p);
-}
 // Scores; those below exp(kLowest), next to the smallest normal number, are 0, and so are those of -inf and NaN.
 constexpr float kLowest = -87.0f;
 __device__ __forceinline__ float sigmoid_score(float l) {

@@ -110,11 +110,10 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows(LinearArgs a) {
 
 template <bool kF16, bool kOutF32, bool kGated, bool kVec>
 cudaError_t launch_rows_nt(const LinearArgs& a, cudaStream_t st) {
-    const int nt = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
+    const int nt = a.T <= 8 ? 1 : 2;
     const dim3 grid((a.N + 15) / 16, (a.T + 8 * nt - 1) / (8 * nt)), block(32 * kRowsWarps);
     if (nt == 1) return launch_with_pdl(linear_rows<kF16, kOutF32, kGated, 1, kVec>, grid, block, 0, st, a);
-    if (nt == 2) return launch_with_pdl(linear_rows<kF16, kOutF32, kGated, 2, kVec>, grid, block, 0, st, a);
-    return launch_with_pdl(linear_rows<kF16, kOutF32, kGated, 4, kVec>, grid, block, 0, st, a);
+    return launch_with_pdl(linear_rows<kF16, kOutF32, kGated, 2, kVec>, grid, block, 0, st, a);
 }
 
 template <bool kF16, bool kOutF32>
@@ -129,23 +128,65 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t st) {
 
 // Operands whose rows do not start at multiples of 16 bytes are copied to rows that do, for the tensor-core
 // kernels (TMA reads rows at such addresses only).
-constexpr int kFewTokens = 32;   // at most this many: linear_rows
+constexpr int kFewTokens = 16;   // at most this many: linear_rows may be taken
 
 static bool straight(long long stride) { return stride % 8 == 0; }
 static long long padded(int K) { return (K + 7) / 8 * 8; }
 
-__global__ void __launch_bounds__(256) realign_rows(const uint16_t* __restrict__ src, long long src_stride, int K,
-                                                    uint16_t* __restrict__ dst, long long dst_stride) {
+// One operand to copy: rows of K elements from any element address to rows at multiples of 16 bytes, zeros beyond K.
+struct Realign {
+    const uint16_t* src;
+    uint16_t* dst;
+    long long src_stride;
+    int rows;
+};
+
+// A thread writes 16 bytes, from five 4-byte words where the row starts in the middle of one (else four).
+__global__ void __launch_bounds__(256) realign_rows(Realign r0, Realign r1, int K, int pieces) {
     pdl_wait();
     pdl_launch_dependents();
-    const uint16_t* s = src + (long long)blockIdx.x * src_stride;
-    uint4* d = reinterpret_cast<uint4*>(dst + (long long)blockIdx.x * dst_stride);
-    for (int c = threadIdx.x; c < (int)(dst_stride / 8); c += blockDim.x) d[c] = load8<false>(s + 8 * c, K - 8 * c);
+    long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long n0 = (long long)r0.rows * pieces;
+    Realign r = r0;
+    if (i >= n0) {
+        i -= n0;
+        r = r1;
+        if (i >= (long long)r.rows * pieces) return;
+    }
+    const int row = (int)(i / pieces), c = 8 * (int)(i - (long long)row * pieces), left = K - c;   // elements left
+    const uint16_t* p = r.src + row * r.src_stride + c;
+    const bool odd = reinterpret_cast<uintptr_t>(p) & 2;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p - (odd ? 1 : 0));   // aligned words
+    uint32_t w[5];
+#pragma unroll
+    for (int u = 0; u < 5; ++u) w[u] = 2 * u - (odd ? 1 : 0) < left && (u < 4 || odd) ? __ldg(q + u) : 0u;
+    uint32_t o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        o[u] = odd ? __funnelshift_r(w[u], w[u + 1], 16) : w[u];
+        if (2 * u + 1 >= left) o[u] = 2 * u < left ? o[u] & 0xffffu : 0u;
+    }
+    reinterpret_cast<uint4*>(r.dst)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Whether linear_rows does it: few tokens, and not longer than the tensor-core kernels would take.  Its time,
+// fitted like theirs: an iteration of its eight warps covers 1024 columns of K and is a load's latency; large
+// weights stream from HBM, which the tensor-core kernels do at the full rate.
+static bool takes_rows(const LinearArgs& a) {
+    if (a.T > kFewTokens) return false;
+    const double bytes = 2.0 * a.rows * a.K, iterations = (a.K + 1023) / 1024;
+    const bool vec = straight(a.w_stride) && straight(a.x_stride);
+    const double step = (a.T <= 8 ? 0.9 : 1.65) * (vec ? 1.0 : 1.6);
+    const double rate = (a.T <= 8 ? 6.4e6 / (1 + 0.015 * a.T) : 4.1e6) / (vec ? 1.0 : 1.8);   // element loads
+    const double rows_us = 1.9 + (iterations * step > bytes / rate ? iterations * step : bytes / rate);
+    const double stream = bytes > 100e6 ? 1.4 + bytes / 6.7e6 : 0.0, loop = linear_tc_us(a);   // past L2: HBM's rate
+    const double copy = straight(a.w_stride) ? straight(a.x_stride) ? 0.0 : 2.0 : 2.0 + bytes / 3e6;
+    return rows_us <= copy + (loop > stream ? loop : stream);
 }
 
 size_t linear_workspace(const LinearArgs& a) {
     size_t n = 256;
-    if (a.T > kFewTokens) {
+    if (!takes_rows(a)) {
         if (!straight(a.w_stride)) n += align_up((size_t)a.rows * padded(a.K) * 2, 256);
         if (!straight(a.x_stride)) n += align_up((size_t)a.T * padded(a.K) * 2, 256);
     }
@@ -155,27 +196,31 @@ size_t linear_workspace(const LinearArgs& a) {
 cudaError_t launch_linear(const LinearArgs& args, cudaStream_t st, unsigned long long* launches) {
     LinearArgs a = args;
     *launches += 1;
-    if (a.T <= kFewTokens) {
+    if (takes_rows(a)) {
         if (a.f16) return a.out_f32 ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);
         return a.out_f32 ? launch_rows<false, true>(a, st) : launch_rows<false, false>(a, st);
     }
-    uint8_t* at = a.ws + 256;
-    const long long stride = padded(a.K);
-    if (!straight(a.w_stride)) {
-        const cudaError_t e = launch_with_pdl(realign_rows, dim3(a.rows), dim3(256), 0, st, static_cast<const uint16_t*>(a.w),
-                                              a.w_stride, a.K, reinterpret_cast<uint16_t*>(at), stride);
+    const bool copy_w = !straight(a.w_stride), copy_x = !straight(a.x_stride);
+    if (copy_w || copy_x) {
+        const long long stride = padded(a.K);
+        uint8_t* at = a.ws + 256;
+        Realign r[2] = {};
+        if (copy_w) {
+            r[0] = Realign{static_cast<const uint16_t*>(a.w), reinterpret_cast<uint16_t*>(at), a.w_stride, a.rows};
+            a.w = at;
+            a.w_stride = stride;
+            at += align_up((size_t)a.rows * stride * 2, 256);
+        }
+        if (copy_x) {
+            r[1] = Realign{static_cast<const uint16_t*>(a.x), reinterpret_cast<uint16_t*>(at), a.x_stride, a.T};
+            a.x = at;
+            a.x_stride = stride;
+        }
+        const int pieces = (int)(stride / 8);
+        const long long threads = ((long long)r[0].rows + r[1].rows) * pieces;
+        const cudaError_t e = launch_with_pdl(realign_rows, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, r[0],
+                                              r[1], a.K, pieces);
         if (e != cudaSuccess) return e;
-        a.w = at;
-        a.w_stride = stride;
-        at += align_up((size_t)a.rows * stride * 2, 256);
-        *launches += 1;
-    }
-    if (!straight(a.x_stride)) {
-        const cudaError_t e = launch_with_pdl(realign_rows, dim3(a.T), dim3(256), 0, st, static_cast<const uint16_t*>(a.x),
-                                              a.x_stride, a.K, reinterpret_cast<uint16_t*>(at), stride);
-        if (e != cudaSuccess) return e;
-        a.x = at;
-        a.x_stride = stride;
         *launches += 1;
     }
     return launch_linear_tc(a, st);

@@ -11,12 +11,30 @@ namespace moe {
 
 #ifdef __CUDACC__
 
-// act(z) in fp32.  kExact (fp32 outputs): CUDA's full-precision functions.  Else the result is rounded
-// to bf16 or fp16 (8 or 11 bits), and the exponential is the hardware one: its relative error,
-// a few 2^-23 and another 2^-24 |z|, disappears in that rounding.
+// act(z) in fp32.  kExact (fp32 outputs): the exponential is good to a few 2^-23.  Else the result is rounded
+// to bf16 or fp16 (8 or 11 bits), and the exponential is the hardware one: its relative error, a few 2^-23 and
+// another 2^-24 |z|, disappears in that rounding.
 template <bool kExact>
 __device__ __forceinline__ float sigmoid_f32(float z) {
-    return kExact ? 1.0f / (1.0f + expf(-z)) : __fdividef(1.0f, 1.0f + __expf(-z));
+    return __fdividef(1.0f, 1.0f + (kExact ? exp_f32(fminf(fmaxf(-z, -88.0f), 88.0f)) : __expf(-z)));
+}
+
+// z Phi(z).  The upper tail of |z| is 0.5 exp(-z^2 / 2) times the scaled complementary error function, for which
+// a polynomial in t = 1 / (1 + 0.43 x), x = |z| / sqrt 2, was fitted here in 64 bits by least squares of the
+// relative error (1e-7 for x up to 9.3; 4e-7 with its terms in fp32), so that small values keep their digits.
+template <bool kExact>
+__device__ __forceinline__ float gelu_f32(float z) {
+    const float x = fminf(fabsf(z), 13.0f), t = __fdividef(1.0f, fmaf(0.43f * 0.70710678f, x, 1.0f));
+    float p = 0.0737080984f;
+    p = fmaf(p, t, -0.310374153f);
+    p = fmaf(p, t, 0.383707111f);
+    p = fmaf(p, t, -0.0857271134f);
+    p = fmaf(p, t, 0.246845185f);
+    p = fmaf(p, t, 0.20495087f);
+    p = fmaf(p, t, 0.244375479f);
+    p = fmaf(p, t, 0.242514606f);
+    const float s = -0.5f * x * x, q = 0.5f * t * p * (kExact ? exp_f32(s) : __expf(s));
+    return z * (z < 0.0f ? q : 1.0f - q);
 }
 
 template <bool kExact>
@@ -24,12 +42,26 @@ __device__ __forceinline__ float apply_act(int act, float z) {
     switch (act) {
         case MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;   // a NaN stays one
         case MOE_ACT_SILU: return z * sigmoid_f32<kExact>(z);
-        // z Phi(z): erfc keeps the relative accuracy where Phi is small
-        case MOE_ACT_GELU: return 0.5f * z * erfcf(-0.70710678f * z);
+        case MOE_ACT_GELU: return gelu_f32<kExact>(z);
         // tanh form: 0.5 z (1 + tanh u) = z / (1 + exp(-2u)), u = sqrt(2/pi) (z + 0.044715 z^3)
         case MOE_ACT_GELU_TANH: return z * sigmoid_f32<kExact>(1.5957691216f * (z + 0.044715f * z * z * z));
         default: return z;
     }
+}
+
+// The same for an array, the choice taken once (unrolled around a switch for each element the code outgrows the
+// instruction cache).
+template <bool kExact, int kCnt>
+__device__ __forceinline__ void apply_act_all(int act, float (&v)[kCnt]) {
+    const auto all = [&](auto one) {
+#pragma unroll
+        for (int j = 0; j < kCnt; ++j) v[j] = one(v[j]);
+    };
+    if (act == MOE_ACT_NONE) return;
+    if (act == MOE_ACT_RELU) all([](float z) { return apply_act<kExact>(MOE_ACT_RELU, z); });
+    else if (act == MOE_ACT_SILU) all([](float z) { return apply_act<kExact>(MOE_ACT_SILU, z); });
+    else if (act == MOE_ACT_GELU) all([](float z) { return apply_act<kExact>(MOE_ACT_GELU, z); });
+    else all([](float z) { return apply_act<kExact>(MOE_ACT_GELU_TANH, z); });
 }
 
 template <bool kF16>

@@ -1,22 +1,23 @@
 // linear_tc.cu -- moe_linear on the 5th-generation tensor cores (more than a few tokens).
 //
-// Both kernels compute D[token][feature] = sum_k x[token][k] w[feature][k] with x rows as the M and w rows
-// as the N side of tcgen05.mma: both are K-major, both come in by TMA as 64-column blocks with the
-// 128-byte swizzle (TMA fills what lies beyond T, N or K with zeros), the fp32 accumulator is in TMEM.
+// Operands are K-major and come in by TMA as 64-column blocks with the 128-byte swizzle (TMA fills what lies
+// beyond T, N or K with zeros); the fp32 accumulators are in TMEM.
 //
-//   linear_pair   large products.  Two CTAs (a cluster) share one 256-token x TN-feature tile: each holds
-//                 128 tokens' rows and half of the weight rows, so a byte of shared memory feeds twice the
-//                 products of a single-CTA tile.  Persistent; while the epilogue empties one accumulator
-//                 the next tile's products go into another.
-//   linear_split  few tiles.  One CTA per 128-token x TN-feature tile and slice of K; the 1..8 CTAs of a
-//                 cluster hold the slices of one tile and add their fp32 partial sums through
-//                 distributed shared memory, in slice order, so that a small product still uses most SMs.
+//   linear_pair   large products.  D[token][feature]: two CTAs (a cluster) share one 256-token x kTN-row tile,
+//                 each holds 128 tokens' rows and half of the weight rows, so a byte of shared memory feeds
+//                 twice the products of a single-CTA tile.  Persistent; while the epilogue empties one
+//                 accumulator the next tile's products go into another.
+//   linear_feat   few tokens, or few tiles.  D[feature][token]: a tile is 128 features x 16..256 tokens of one
+//                 CTA.  Persistent over the tiles where they are many (a stream of the weights); where they are
+//                 few, the 2..8 CTAs of a cluster take slices of K of one tile and add their fp32 partial sums
+//                 through distributed shared memory, in slice order, so that a small product uses most SMs.
 //
 // fp32 outputs: the tensor cores truncate when they add to the accumulator (about half a unit of 2^-23 of
 // the running sum at each 16-column step, always towards zero), so after kChunk blocks the epilogue
 // takes the partial sum into registers and adds the next in ordinary fp32.  For 16-bit outputs that
 // error is far below the rounding of the output, and the whole of K stays in the accumulator.
 #include <atomic>
+#include <type_traits>
 
 #include "linear_common.cuh"
 
@@ -26,14 +27,15 @@ namespace {
 constexpr int kLK = 64;                 // columns of K per block: one 128-byte swizzle row
 constexpr int kLM = 128;                // token rows a CTA holds
 constexpr int kChunk = 8;               // blocks summed in the accumulator for fp32 outputs
-constexpr int kEpiWarps = 8;            // two warpgroups, each half of the columns
-constexpr int kTcThreads = 32 * (4 + kEpiWarps);   // warps 0..3: producer, issuer, TMEM, spare
+// Threads: four warps (producer, issuer, TMEM, spare) and `groups` warpgroups of the epilogue, each with its share of
+// a tile's columns.  Four groups where the tile is wide: short K loops leave the time to the epilogue.
+__host__ __device__ constexpr int tc_threads(int groups) { return 128 * (1 + groups); }
 
-constexpr int kPairStages = 6;
+constexpr int kPairMaxStages = 6;
 constexpr int kStageBuf = 128 * 128;    // a warpgroup's output staging: 128 rows of 128 bytes
 
 struct PairSmem {
-    uint64_t full[kPairStages], empty[kPairStages];
+    uint64_t full[kPairMaxStages], empty[kPairMaxStages];
     uint64_t acc_full[4], acc_empty[4];
     uint32_t tmem;
     int abort;
@@ -107,6 +109,48 @@ __device__ __forceinline__ uint4* stage_piece(uint8_t* buf, int r, int piece) {
     return reinterpret_cast<uint4*>(buf + r * 128 + ((piece ^ (r & 7)) << 4));
 }
 
+template <int kCols>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[kCols]) {   // the wait is the caller's
+    static_assert(kCols == 8 || kCols == 16 || kCols == 32, "columns of a TMEM load");
+    if constexpr (kCols == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    else if constexpr (kCols == 16) tmem_ld16(taddr, r);
+    else tmem_ld32(taddr, r);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
+}
+
+// fp32 outputs in several chunks: adds this chunk's kCols columns (of each of G accumulators, kNext columns apart)
+// to the running sums; after the last chunk the sums go back to TMEM, where the epilogue finds the products of
+// one-chunk tiles too.
+template <int G, int kCols, int kNext>
+__device__ __forceinline__ void add_chunk(uint32_t acc, float (&sum)[G * kCols], bool first, bool last) {
+    constexpr int kB = kCols < 32 ? kCols : 32;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < kCols; j += kB) {
+            uint32_t q[kB];
+            tmem_ld_cols<kB>(acc + g * kNext + j, q);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < kB; ++u)
+                sum[g * kCols + j + u] = first ? __uint_as_float(q[u]) : sum[g * kCols + j + u] + __uint_as_float(q[u]);
+        }
+    if (last) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int j = 0; j < kCols; j += 8) tmem_st8(acc + g * kNext + j, &sum[g * kCols + j]);
+        tmem_st_wait();
+    }
+}
+
 struct TcArgs {
     LinearArgs l;
     int tiles_m, tiles_n, nkb;
@@ -124,39 +168,43 @@ __device__ __forceinline__ void tile_at(int i, int tiles_m, int tiles_n, int* m,
     *n = j / h;
 }
 
-// Adds the residual to 32 outputs (features n0.. of token t; valid of them exist) held as fp32.
-template <bool kF16, bool kOutF32>
-__device__ __forceinline__ void add_residual(const TcArgs& a, long long t, int n0, int valid, float (&v)[32]) {
-    if (kOutF32) {
-        const float* p = static_cast<const float*>(a.l.residual) + t * a.l.r_stride + n0;
-        if (a.r_vec && valid == 32) {
+// The residual of 32 outputs (features n0.. of token t; `valid` of them exist) as stored, zeros beyond.
+template <bool kOutF32>
+struct Residual32 {
+    uint4 q[kOutF32 ? 8 : 4];
+};
+template <bool kOutF32>
+__device__ __forceinline__ void load_residual32(const TcArgs& a, long long t, int n0, int valid, Residual32<kOutF32>& r) {
+    constexpr int kVecs = kOutF32 ? 8 : 4, kPer = kOutF32 ? 4 : 8;
+    using Elem = typename std::conditional<kOutF32, uint32_t, uint16_t>::type;
+    const Elem* p = static_cast<const Elem*>(a.l.residual) + t * a.l.r_stride + n0;
+    if (a.r_vec && valid == 32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 q = *reinterpret_cast<const float4*>(p + 4 * i);
-                v[4 * i] += q.x; v[4 * i + 1] += q.y; v[4 * i + 2] += q.z; v[4 * i + 3] += q.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < valid) v[i] += p[i];
-        }
+        for (int i = 0; i < kVecs; ++i) r.q[i] = *reinterpret_cast<const uint4*>(p + kPer * i);
     } else {
-        const uint16_t* p = static_cast<const uint16_t*>(a.l.residual) + t * a.l.r_stride + n0;
-        if (a.r_vec && valid == 32) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 q = *reinterpret_cast<const uint4*>(p + 8 * i);
-                const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+        for (int i = 0; i < kVecs; ++i) {
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[8 * i + 2 * j] += elem_f32<kF16>((uint16_t)(u[j] & 0xffffu));
-                    v[8 * i + 2 * j + 1] += elem_f32<kF16>((uint16_t)(u[j] >> 16));
-                }
+            for (int j = 0; j < kPer; ++j)
+                if (kPer * i + j < valid) w[j * 4 / kPer] |= (uint32_t)p[kPer * i + j] << (kOutF32 ? 0 : 16 * (j % 2));
+            r.q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+template <bool kF16, bool kOutF32>
+__device__ __forceinline__ void add_residual32(const Residual32<kOutF32>& r, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < (kOutF32 ? 8 : 4); ++i) {
+        const uint32_t u[4] = {r.q[i].x, r.q[i].y, r.q[i].z, r.q[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (kOutF32) {
+                v[(4 * i + j) % 32] += __uint_as_float(u[j]);
+            } else {
+                v[(8 * i + 2 * j) % 32] += elem_f32<kF16>((uint16_t)(u[j] & 0xffffu));
+                v[(8 * i + 2 * j + 1) % 32] += elem_f32<kF16>((uint16_t)(u[j] >> 16));
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < valid) v[i] += elem_f32<kF16>(p[i]);
         }
     }
 }
@@ -169,23 +217,74 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
+template <bool kOutF32>
+using OutElem = typename std::conditional<kOutF32, float, uint16_t>::type;
+
+// The residual of one feature n of kCnt consecutive tokens from t0, as stored (0 beyond the last token).
+template <bool kOutF32, int kCnt>
+__device__ __forceinline__ void load_residual(const LinearArgs& l, long long t0, int n, OutElem<kOutF32> (&r)[kCnt]) {
+    const long long left = l.T - t0;
+    const int cnt = n < l.N && left > 0 ? (int)min((long long)kCnt, left) : 0;
+    const OutElem<kOutF32>* p = static_cast<const OutElem<kOutF32>*>(l.residual) + t0 * l.r_stride + n;
+#pragma unroll
+    for (int j = 0; j < kCnt; ++j) {
+        r[j] = 0;
+        if (j < cnt) r[j] = *p;
+        p += l.r_stride;
+    }
+}
+
+// Bias, activation, residual (r, as stored) and store of one feature n of kCnt consecutive tokens from t0 (z: products,
+// u: the up projection's).
+template <bool kOutF32, bool kGated, int kCnt, int kUp>
+__device__ __forceinline__ void finish_column(const LinearArgs& l, long long t0, int n, float b0, float b1,
+                                              float (&z)[kCnt], const float (&u)[kUp], const OutElem<kOutF32> (&r)[kCnt]) {
+    const int cnt = (int)min((long long)kCnt, l.T - t0);
+#pragma unroll
+    for (int j = 0; j < kCnt; ++j) z[j] += b0;
+    if (kGated) {
+#pragma unroll
+        for (int j = 0; j < kCnt; ++j) z[j] = z[j] * sigmoid_f32<kOutF32>(z[j]) * (u[kGated ? j : 0] + b1);
+    } else {
+        apply_act_all<kOutF32>(l.act, z);
+    }
+    if (l.residual) {
+#pragma unroll
+        for (int j = 0; j < kCnt; ++j) {
+            if constexpr (kOutF32) z[j] += r[j];
+            else z[j] += l.f16 ? elem_f32<true>(r[j]) : elem_f32<false>(r[j]);
+        }
+    }
+    OutElem<kOutF32>* y = static_cast<OutElem<kOutF32>*>(l.y) + t0 * l.y_stride + n;
+#pragma unroll
+    for (int j = 0; j < kCnt; ++j) {
+        if (j < cnt) {
+            if constexpr (kOutF32) *y = z[j];
+            else *y = l.f16 ? elem_from_f32<true>(z[j]) : elem_from_f32<false>(z[j]);
+        }
+        y += l.y_stride;
+    }
+}
+
 // kTN: weight rows of a tile (256, or 128 with fp32 outputs so that a thread's running sums fit its
 // registers); with kGated half of them are gate rows and half the up rows of the same features.
 template <bool kF16, bool kOutF32, bool kGated, int kTN>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(tc_threads(kGated ? 2 : 4), 1)
     linear_pair(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_y, TcArgs a) {
     constexpr int kBRows = kTN / 2;                          // weight rows a CTA holds
     constexpr int kABytes = kLM * 128, kBBytes = kBRows * 128, kStage = kABytes + kBBytes;
     constexpr int kBufs = 512 / kTN;                         // accumulators in TMEM
     constexpr int kFeat = kGated ? kTN / 2 : kTN;            // outputs of a tile
-    constexpr int kHalf = kFeat / 2;                         // outputs a warpgroup handles
+    constexpr int kGroups = kGated ? 2 : 4;                  // warpgroups of the epilogue
+    constexpr int kHalf = kFeat / kGroups;                   // outputs a warpgroup handles
+    constexpr int kPairStages = kGroups == 2 ? 6 : 5;
     constexpr int kGrp = kOutF32 ? 32 : 64;                  // outputs of one staging row (128 bytes)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t* staging = smem + kPairStages * kStage;          // two buffers, one per warpgroup
-    float* s_bias = reinterpret_cast<float*>(staging + 2 * kStageBuf);   // [warpgroup][2][64]
-    PairSmem* sh = reinterpret_cast<PairSmem*>(s_bias + 2 * 128);
+    uint8_t* staging = smem + kPairStages * kStage;          // a buffer per warpgroup
+    float* s_bias = reinterpret_cast<float*>(staging + kGroups * kStageBuf);   // [warpgroup][gate, up][64]
+    PairSmem* sh = reinterpret_cast<PairSmem*>(s_bias + 256);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
@@ -204,7 +303,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(&sh->acc_full[i], 1);
-            mbar_init(&sh->acc_empty[i], 2 * kEpiWarps);
+            mbar_init(&sh->acc_empty[i], 2 * 4 * kGroups);
         }
         sh->abort = 0;
         fence_barrier_init();
@@ -284,53 +383,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok && lane == 0) { *abort = 1; set_status(status, MOE_STATUS_TIMEOUT); }
     } else if (warp >= 4) {
         // ------------------------------ epilogue ------------------------------
-        const int ew = warp - 4, half = ew >> 2, quarter = ew & 3;   // columns, TMEM lanes
+        const int ew = warp - 4, half = ew >> 2, quarter = ew & 3;   // share of the columns, TMEM lanes
         const int r = 32 * quarter + lane;                           // token row in the CTA's tile
         uint8_t* stg = staging + half * kStageBuf;
-        float* sb = s_bias + half * 128;
+        float* sb = s_bias + half * (256 / kGroups);
         const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
         const bool issuer = (ew & 3) == 0 && lane == 0;              // stores of this warpgroup
         int buf = 0;
         uint32_t fph = 0;
         bool ok = true;
+        // the residual of the next 32 outputs is loaded while these are worked on (16-bit; fp32 residuals, whose registers
+        // the running sums need, when they are added)
+        Residual32<kOutF32> res = {};
+        const auto fetch = [&](int tile, int col) {
+            int m, n;
+            tile_at(tile, a.tiles_m, a.tiles_n, &m, &n);
+            const long long t = (long long)m * 2 * kLM + (int)rank * kLM + r;
+            const int nj = n * kFeat + half * kHalf + col;
+            if (t < a.l.T && nj < a.l.N) load_residual32<kOutF32>(a, t, nj, min(32, a.l.N - nj), res);
+        };
+        if (a.l.residual && !kOutF32) fetch(cluster, 0);
         for (int i = cluster; i < tiles && ok; i += clusters) {
             int m, n;
             tile_at(i, a.tiles_m, a.tiles_n, &m, &n);
             const long long t0 = (long long)m * 2 * kLM + (int)rank * kLM;
             const int n0 = n * kFeat + half * kHalf;
+            const uint32_t cols = tmem + lane_addr + half * kHalf;
             float sum[kOutF32 ? (kGated ? 2 : 1) * kHalf : 1];
             for (int c = 0; c < nch; ++c) {
                 // one answer for the warpgroup, so that its barriers below are reached by all or none
                 const bool got = mbar_wait(&sh->acc_full[buf], fph, abort);
                 if (named_bar_or(1 + half, 128, !got)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t acc = tmem + lane_addr + buf * kTN + half * kHalf;
-                if (kOutF32) {
-#pragma unroll
-                    for (int g = 0; g < (kGated ? 2 : 1); ++g)
-#pragma unroll
-                        for (int j = 0; j < kHalf; j += 32) {
-                            uint32_t q[32];
-                            tmem_ld32(acc + g * kFeat + j, q);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int u = 0; u < 32; ++u)
-                                sum[g * kHalf + j + u] =
-                                    c == 0 ? __uint_as_float(q[u]) : sum[g * kHalf + j + u] + __uint_as_float(q[u]);
-                        }
+                if constexpr (kOutF32) {
+                    if (nch > 1) add_chunk<kGated ? 2 : 1, kHalf, kFeat>(cols + buf * kTN, sum, c == 0, c == nch - 1);
                 }
-                if (kOutF32 || c < nch - 1) {   // (16-bit outputs: one chunk, released below)
+                if (c < nch - 1) {   // (the last accumulator is released below)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_release(&sh->acc_empty[buf], 0);
+                    if (++buf == kBufs) { buf = 0; fph ^= 1; }
                 }
-                if (c < nch - 1 && ++buf == kBufs) { buf = 0; fph ^= 1; }
             }
             if (!ok) break;
-            const uint32_t acc = tmem + lane_addr + buf * kTN + half * kHalf;
-            const bool row_in = t0 + r < a.l.T;
-            // 128 bytes of outputs a row at a time
-#pragma unroll
+            const uint32_t acc = cols + buf * kTN;
+            // 128 bytes of outputs a row at a time (rolled: the code of every activation, unrolled for the whole tile,
+            // does not fit the instruction cache)
+#pragma unroll 1
             for (int g0 = 0; g0 < kHalf; g0 += kGrp) {
                 if (issuer) bulk_wait_read();         // the previous store has read the buffer
                 if (a.l.bias && (r & 63) < kGrp && (kGated || r < 64)) {   // bias of these outputs (and of their up rows)
@@ -338,26 +437,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     sb[r] = nb < a.l.N ? __ldg(a.l.bias + (r < 64 ? 0 : a.l.N) + nb) : 0.0f;
                 }
                 named_bar_sync(1 + half, 128);
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < kGrp; j += 32) {
-                    const int nj = n0 + g0 + j, valid = max(0, min(32, a.l.N - nj));
                     float v[32], up[32];
-                    if (kOutF32) {
+                    uint32_t q[32], p[32];
+                    tmem_ld32(acc + g0 + j, q);
+                    if (kGated) tmem_ld32(acc + kFeat + g0 + j, p);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) {
-                            v[u] = sum[g0 + j + u];
-                            if (kGated) up[u] = sum[(kGated ? kHalf : 0) + g0 + j + u];
-                        }
-                    } else {
-                        uint32_t q[32], p[32];
-                        tmem_ld32(acc + g0 + j, q);
-                        if (kGated) tmem_ld32(acc + kFeat + g0 + j, p);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int u = 0; u < 32; ++u) {
-                            v[u] = __uint_as_float(q[u]);
-                            if (kGated) up[u] = __uint_as_float(p[u]);
-                        }
+                    for (int u = 0; u < 32; ++u) {
+                        v[u] = __uint_as_float(q[u]);
+                        if (kGated) up[u] = __uint_as_float(p[u]);
                     }
                     if (a.l.bias) {
 #pragma unroll
@@ -369,11 +459,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (kGated) {
 #pragma unroll
                         for (int u = 0; u < 32; ++u) v[u] = v[u] * sigmoid_f32<kOutF32>(v[u]) * up[u];
-                    } else if (a.l.act != MOE_ACT_NONE) {
-#pragma unroll
-                        for (int u = 0; u < 32; ++u) v[u] = apply_act<kOutF32>(a.l.act, v[u]);
+                    } else {
+                        apply_act_all<kOutF32>(a.l.act, v);
                     }
-                    if (a.l.residual && row_in) add_residual<kF16, kOutF32>(a, t0 + r, nj, valid, v);
+                    if (a.l.residual) {
+                        if (kOutF32) fetch(i, g0 + j);
+                        add_residual32<kF16, kOutF32>(res, v);
+                        if (kOutF32) {}
+                        else if (g0 + j + 32 < kHalf) fetch(i, g0 + j + 32);
+                        else if (i + clusters < tiles) fetch(i + clusters, 0);
+                    }
                     if (kOutF32) {
 #pragma unroll
                         for (int u = 0; u < 8; ++u)
@@ -387,7 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                            pack2<kF16>(v[8 * u + 4], v[8 * u + 5]), pack2<kF16>(v[8 * u + 6], v[8 * u + 7]));
                     }
                 }
-                if (!kOutF32 && g0 + kGrp >= kHalf) {   // the accumulator has been read: the issuer may reuse it
+                if (g0 + kGrp >= kHalf) {   // the accumulator has been read: the issuer may reuse it
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_release(&sh->acc_empty[buf], 0);
@@ -437,227 +532,311 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ---------------------------------------------------------------------------------------------------------
 
-struct SplitSmem {
-    uint64_t full[8], empty[8];
+constexpr int kFeatStages = 12;
+struct FeatSmem {
+    uint64_t full[kFeatStages], empty[kFeatStages];
     uint64_t acc_full[2], acc_empty[2];
+    uint64_t joined;           // the other slices' partial sums have arrived
     uint32_t tmem;
     int abort;
 };
 
-__device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
+// Contiguous bytes from this CTA's shared memory to another's, counted on a barrier there (both shared::cluster).
+__device__ __forceinline__ void bulk_s2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
-template <int kTN> struct SplitShape {
-    static constexpr int kStage = kLM * 128 + kTN * 128;
-    static constexpr int kStages = kTN == 128 ? 6 : 8;
-    static constexpr int kPitch = kTN + 4;                  // floats of a partial-sum row
-    static constexpr int kBytes = 1024 + kStages * kStage + (int)sizeof(SplitSmem);
-    static_assert(kLM * kPitch * 4 <= kStages * kStage, "the partial sums reuse the operand ring");
+// Sums the slices' partial sums of kCnt tokens of feature f, in slice order, and finishes them.  own: this CTA's
+// sums of these tokens; in: the same of slice 0 in its inbound buffer; rows of 128 features.
+template <bool kOutF32, bool kGated, int kCnt>
+__device__ __forceinline__ void join_slices(const LinearArgs& l, const float* own, int own_g, const float* in, int in_g,
+                                            int slices, int rank, long long t, int n, float b0, float b1) {
+    float v[kCnt] = {}, up[kCnt] = {};
+    OutElem<kOutF32> res[kCnt] = {};
+    if (l.residual) load_residual<kOutF32, kCnt>(l, t, n, res);
+    for (int q = 0; q < slices; ++q) {
+        const float* p = q == rank ? own : in + q * (kGated ? 2 : 1) * in_g;
+        const int gg = q == rank ? own_g : in_g;
+#pragma unroll
+        for (int u = 0; u < kCnt; ++u) {
+            v[u] += p[u * kLM];
+            if (kGated) up[u] += p[gg + u * kLM];
+        }
+    }
+    finish_column<kOutF32, kGated, kCnt>(l, t, n, b0, b1, v, up, res);
+}
+
+// Blocks of 64 columns to a stage of the ring.  Waiting for a stage, issuing its products and releasing it cost
+// the issuer and the producer about 0.1 us whatever its size, so small blocks share a stage (one weight tile of
+// 2048 columns: 8.7 us with one block of 16 tokens to a stage, 6.9 with two, 6.1 with four; of 128 tokens 10.6
+// and 9.3 with two).
+__host__ __device__ constexpr int feat_sub(int block) { return block <= 20480 ? 4 : block <= 36864 ? 2 : 1; }
+
+__host__ __device__ constexpr int feat_groups(int tokens) { return tokens >= 64 ? 4 : 2; }   // warpgroups of the epilogue
+
+struct FeatArgs {
+    LinearArgs l;
+    int tiles_n, tiles_t, nkb, slices, stages;
+    int ring;          // bytes of the operand ring (with slices: at least of a tile's partial sums)
 };
 
-template <bool kF16, bool kOutF32, bool kGated, int kTN>
-__global__ void __launch_bounds__(kTcThreads, 1)
-    linear_split(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, TcArgs a) {
-    using Sh = SplitShape<kTN>;
-    constexpr int kStage = Sh::kStage, kStages = Sh::kStages, kPitch = Sh::kPitch;
-    constexpr int kFeat = kGated ? kTN / 2 : kTN;
-    constexpr int kCols = kTN / 2;                           // accumulator columns a warpgroup takes
+// Weight rows as the M side: lane = feature, column = token, so a warp stores 32 consecutive features of a
+// token at once whatever the alignment of y, and a tile costs as many token columns as there are tokens.
+// kTT: tokens of a tile.  kGated: a tile has 128 gate rows and the 128 up rows of the same features, each with
+// its own accumulator.
+template <bool kOutF32, bool kGated, int kTT>
+__global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
+    linear_feat(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, FeatArgs a) {
+    constexpr int G = kGated ? 2 : 1;
+    constexpr int kABytes = G * kLM * 128, kBlock = kABytes + kTT * 128, kSub = feat_sub(kBlock), kStage = kSub * kBlock;
+    constexpr int kGroups = feat_groups(kTT), kThreads = tc_threads(kGroups);
+    constexpr int kHalf = kTT / kGroups;                     // tokens a warpgroup handles
+    constexpr int kBlk = kHalf < 16 ? kHalf : 16;            // of them, at a time
+    constexpr int kAcc = G * kTT;                            // TMEM columns of a tile's accumulators
+    constexpr int kBufs = 2 * kAcc <= 512 ? 2 : 1;
+    constexpr int kTmem = kBufs * kAcc <= 32 ? 32 : kBufs * kAcc;
+    static_assert((kTmem & (kTmem - 1)) == 0 && kTmem <= 512, "TMEM columns");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    SplitSmem* sh = reinterpret_cast<SplitSmem*>(smem + kStages * kStage);
-    float* part = reinterpret_cast<float*>(smem);
+    __shared__ FeatSmem sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int slices = gridDim.x, rank = blockIdx.x;         // the cluster spans x
-    const int m = blockIdx.z, n = blockIdx.y;
-    const int kb0 = (int)((long long)a.nkb * rank / slices), kb1 = (int)((long long)a.nkb * (rank + 1) / slices);
-    const int chunk = kOutF32 ? kChunk : a.nkb, nch = (kb1 - kb0 + chunk - 1) / chunk;
+    const int S = a.slices, rank = S > 1 ? (int)cluster_ctarank() : 0, stages = a.stages;
+    // slices > 1: this CTA's partial sums [G][kTT][128 features] take the ring's place, those of the other slices
+    // for its share of the tokens arrive in [slice][G][per][128]
+    float* own = reinterpret_cast<float*>(smem);
+    float* inbound = reinterpret_cast<float*>(smem + a.ring);
+    const int per = kTT / S;                                 // tokens of the share
+    const int first = S > 1 ? blockIdx.x / S : blockIdx.x, step = S > 1 ? INT32_MAX / 2 : (int)gridDim.x;
+    const int tiles = a.tiles_n * a.tiles_t;
+    const int kb0 = (int)((long long)a.nkb * rank / S), kb1 = (int)((long long)a.nkb * (rank + 1) / S);
+    const int chunk = kOutF32 ? kChunk / kSub : a.nkb, nch = (kb1 - kb0 + chunk - 1) / chunk;
     int* status = reinterpret_cast<int*>(a.l.ws);
-    volatile int* abort = &sh->abort;
+    volatile int* abort = &sh.abort;
 
     if (threadIdx.x == 0) {
         prefetch_tmap(&tm_x);
         prefetch_tmap(&tm_w);
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh->full[i], 1);
-            mbar_init(&sh->empty[i], 1);
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh->acc_full[i], 1);
-            mbar_init(&sh->acc_empty[i], kEpiWarps);
+        for (int i = 0; i < kBufs; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 4 * kGroups);
         }
-        sh->abort = 0;
+        mbar_init(&sh.joined, 1);
+        sh.abort = 0;
         fence_barrier_init();
+        if (S > 1) mbar_arrive_expect_tx(&sh.joined, (S - 1) * G * per * kLM * 4);
     }
     if (warp == 2) {
-        tmem_alloc(&sh->tmem, 2 * kTN);
+        tmem_alloc(&sh.tmem, kTmem);
         tmem_relinquish();
+    }
+    if (warp == 3 && lane < stages && kb0 + lane < kb1) {
+        // warm L2 with the first weight blocks while the previous kernel on the stream finishes (only a hint:
+        // what that kernel may still write is read after the wait below)
+        const int n0 = first % a.tiles_n * kLM;
+        for (int u = 0; u < kSub; ++u) {
+            prefetch_l2_tile(&tm_w, ((kb0 + lane) * kSub + u) * kLK, n0);
+            if (kGated) prefetch_l2_tile(&tm_w, ((kb0 + lane) * kSub + u) * kLK, a.l.N + n0);
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh->tmem;
+    const uint32_t tmem = sh.tmem;
+    if (S > 1) cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();
+    if (S > 1) cluster_wait();   // every CTA of the cluster runs: its shared memory may be written
 
     if (warp == 0) {
         int s = 0;
         uint32_t ph = 1;
         bool ok = true;
-        const int t0 = m * kLM, w0 = n * kFeat;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait_warp(&sh->empty[s], ph, abort)) { ok = false; break; }
-            if (elect_one()) {
-                uint8_t* st = smem + s * kStage;
-                mbar_arrive_expect_tx(&sh->full[s], kStage);
-                tma_load_2d(st, &tm_x, kb * kLK, t0, &sh->full[s]);
-                tma_load_2d(st + kLM * 128, &tm_w, kb * kLK, w0, &sh->full[s]);
-                if (kGated) tma_load_2d(st + kLM * 128 + kFeat * 128, &tm_w, kb * kLK, a.l.N + w0, &sh->full[s]);
+        for (int i = first; i < tiles && ok; i += step) {
+            const int n0 = i % a.tiles_n * kLM, t0 = i / a.tiles_n * kTT;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_warp(&sh.empty[s], ph, abort)) { ok = false; break; }
+                if (elect_one()) {
+                    uint8_t* st = smem + s * kStage;
+                    mbar_arrive_expect_tx(&sh.full[s], kStage);
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u) {
+                        const int c = (kb * kSub + u) * kLK;
+                        uint8_t* at = st + u * kBlock;
+                        tma_load_2d(at, &tm_w, c, n0, &sh.full[s]);
+                        if (kGated) tma_load_2d(at + kLM * 128, &tm_w, c, a.l.N + n0, &sh.full[s]);
+                        tma_load_2d(at + kABytes, &tm_x, c, t0, &sh.full[s]);
+                    }
+                }
+                if (++s == stages) { s = 0; ph ^= 1; }
             }
-            if (++s == kStages) { s = 0; ph ^= 1; }
         }
         if (!ok && lane == 0) { *abort = 1; set_status(status, MOE_STATUS_TIMEOUT); }
     } else if (warp == 1) {
-        const uint32_t idesc = idesc_f16kind(kF16, kLM, kTN);
+        const uint32_t idesc = idesc_f16kind(a.l.f16, kLM, kTT);
         int s = 0, buf = 0;
         uint32_t ph = 0, eph = 1;
         bool ok = true;
-        for (int c = 0; c < nch && ok; ++c) {
-            if (!mbar_wait_warp(&sh->acc_empty[buf], eph, abort)) { ok = false; break; }
-            tc_fence_after();
-            const int f = kb0 + c * chunk, k1 = min(kb1, f + chunk);
-            for (int kb = f; kb < k1; ++kb) {
-                if (!mbar_wait_warp(&sh->full[s], ph, abort)) { ok = false; break; }
+        for (int i = first; i < tiles && ok; i += step) {
+            for (int c = 0; c < nch && ok; ++c) {
+                if (!mbar_wait_warp(&sh.acc_empty[buf], eph, abort)) { ok = false; break; }
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t sa = smem_u32(smem + s * kStage);
-                    const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + kLM * 128);
+                const int f = kb0 + c * chunk, k1 = min(kb1, f + chunk);
+                const uint32_t d = tmem + buf * kAcc;
+                for (int kb = f; kb < k1; ++kb) {
+                    if (!mbar_wait_warp(&sh.full[s], ph, abort)) { ok = false; break; }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t sa = smem_u32(smem + s * kStage);
 #pragma unroll
-                    for (int k = 0; k < kLK / 16; ++k)
-                        tc_mma_f16kind<false>(tmem + buf * kTN, ad + 2 * k, bd + 2 * k, idesc, kb > f || k > 0);
-                    tc_commit(&sh->empty[s]);
-                    if (kb == k1 - 1) tc_commit(&sh->acc_full[buf]);
+                        for (int u = 0; u < kSub; ++u) {
+                            const uint64_t bd = sw128_desc(sa + u * kBlock + kABytes);
+#pragma unroll
+                            for (int g = 0; g < G; ++g) {
+                                const uint64_t ad = sw128_desc(sa + u * kBlock + g * kLM * 128);
+#pragma unroll
+                                for (int k = 0; k < kLK / 16; ++k)
+                                    tc_mma_f16kind<false>(d + g * kTT, ad + 2 * k, bd + 2 * k, idesc, kb > f || u > 0 || k > 0);
+                            }
+                        }
+                        tc_commit(&sh.empty[s]);
+                        if (kb == k1 - 1) tc_commit(&sh.acc_full[buf]);
+                    }
+                    __syncwarp();
+                    if (++s == stages) { s = 0; ph ^= 1; }
                 }
-                __syncwarp();
-                if (++s == kStages) { s = 0; ph ^= 1; }
+                if (++buf == kBufs) { buf = 0; eph ^= 1; }
             }
-            if (++buf == 2) { buf = 0; eph ^= 1; }
         }
         if (!ok && lane == 0) { *abort = 1; set_status(status, MOE_STATUS_TIMEOUT); }
     } else if (warp >= 4) {
-        const int ew = warp - 4, half = ew >> 2, quarter = ew & 3, r = 32 * quarter + lane;
-        float sum[kCols];
+        const int ew = warp - 4, half = ew >> 2, quarter = ew & 3, r = 32 * quarter + lane;   // feature in the tile
         int buf = 0;
         uint32_t fph = 0;
         bool ok = true;
-        for (int c = 0; c < nch; ++c) {
-            const bool got = mbar_wait(&sh->acc_full[buf], fph, abort);
-            if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + buf * kTN + half * kCols;
-#pragma unroll
-            for (int j = 0; j < kCols; j += 32) {
-                uint32_t q[32];
-                tmem_ld32(acc + j, q);
+        // the residual of the next kBlk outputs is loaded while these are worked on
+        const bool has_res = a.l.residual && S == 1;
+        OutElem<kOutF32> res[kBlk] = {};
+        if (has_res && first < tiles)
+            load_residual<kOutF32, kBlk>(a.l, (long long)(first / a.tiles_n) * kTT + half * kHalf, first % a.tiles_n * kLM + r, res);
+        for (int i = first; i < tiles && ok; i += step) {
+            const int n = i % a.tiles_n * kLM + r;
+            const long long t0 = (long long)(i / a.tiles_n) * kTT + half * kHalf;
+            const uint32_t cols = tmem + ((uint32_t)(32 * quarter) << 16) + half * kHalf;
+            float sum[kOutF32 ? G * kHalf : 1];
+            for (int c = 0; c < nch; ++c) {
+                const bool got = mbar_wait_warp(&sh.acc_full[buf], fph, abort);
+                if (!got) { ok = false; break; }
+                tc_fence_after();
+                if constexpr (kOutF32) {
+                    if (nch > 1) add_chunk<G, kHalf, kTT>(cols + buf * kAcc, sum, c == 0, c == nch - 1);
+                }
+                if (c < nch - 1) {   // (the last accumulator is released below)
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+                    if (++buf == kBufs) { buf = 0; fph ^= 1; }
+                }
+            }
+            if (!ok) break;
+            const uint32_t acc = cols + buf * kAcc;
+            const float b0 = a.l.bias && n < a.l.N ? __ldg(a.l.bias + n) : 0.0f;
+            const float b1 = kGated && a.l.bias && n < a.l.N ? __ldg(a.l.bias + a.l.N + n) : 0.0f;
+#pragma unroll 1
+            for (int j = 0; j < kHalf; j += kBlk) {   // rolled: see linear_pair
+                float v[kBlk], up[kGated ? kBlk : 1];
+                uint32_t q[kBlk], p[kBlk];
+                tmem_ld_cols<kBlk>(acc + j, q);
+                if (kGated) tmem_ld_cols<kBlk>(acc + kTT + j, p);
                 tmem_ld_wait();
 #pragma unroll
-                for (int u = 0; u < 32; ++u)
-                    sum[j + u] = c == 0 ? __uint_as_float(q[u]) : sum[j + u] + __uint_as_float(q[u]);
+                for (int u = 0; u < kBlk; ++u) {
+                    v[u] = __uint_as_float(q[u]);
+                    if (kGated) up[kGated ? u : 0] = __uint_as_float(p[u]);
+                }
+                if (S > 1) {
+                    // the ring is free: this CTA's products are complete, in order, with the last accumulator
+#pragma unroll
+                    for (int u = 0; u < kBlk; ++u) {
+                        own[(half * kHalf + j + u) * kLM + r] = v[u];
+                        if (kGated) own[(kTT + half * kHalf + j + u) * kLM + r] = up[kGated ? u : 0];
+                    }
+                } else {
+                    OutElem<kOutF32> now[kBlk];
+#pragma unroll
+                    for (int u = 0; u < kBlk; ++u) now[u] = res[u];
+                    if (has_res) {
+                        if (j + kBlk < kHalf) {
+                            load_residual<kOutF32, kBlk>(a.l, t0 + j + kBlk, n, res);
+                        } else if (i + step < tiles) {
+                            const int ni = i + step;
+                            load_residual<kOutF32, kBlk>(a.l, (long long)(ni / a.tiles_n) * kTT + half * kHalf,
+                                                         ni % a.tiles_n * kLM + r, res);
+                        }
+                    }
+                    if (n < a.l.N) finish_column<kOutF32, kGated, kBlk>(a.l, t0 + j, n, b0, b1, v, up, now);
+                }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->acc_empty[buf]);
-            if (++buf == 2) { buf = 0; fph ^= 1; }
+            if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+            if (++buf == kBufs) { buf = 0; fph ^= 1; }
         }
         if (!ok && lane == 0) { *abort = 1; set_status(status, MOE_STATUS_TIMEOUT); }
-        // the last accumulator is complete: every product has read its operands, and the ring is free
-        // (with several chunks too: commits complete in order)
-        if (ok) {
-#pragma unroll
-            for (int j = 0; j < kCols; j += 4)
-                *reinterpret_cast<float4*>(part + r * kPitch + half * kCols + j) =
-                    make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
-        }
+        if (S > 1 && ok) fence_proxy_async_smem();   // the partial sums, before they are copied
     }
     __syncthreads();
+    if (S > 1) {
+        // the cluster's CTAs share out the tile's tokens: each sends the others theirs
+        if (warp == 4 && !*abort && elect_one()) {
+            for (int q = 1; q < S; ++q) {
+                const int to = (rank + q) % S;
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    bulk_s2s(map_to_rank(inbound + (rank * G + g) * per * kLM, to), own + (g * kTT + to * per) * kLM, per * kLM * 4,
+                             map_to_rank(&sh.joined, to));
+            }
+        }
+        __syncwarp();
+        const bool got = mbar_wait_warp(&sh.joined, 0, abort);
+        if (!got && lane == 0) { *abort = 1; set_status(status, MOE_STATUS_TIMEOUT); }
+        cluster_arrive();   // everything for this CTA has arrived; it leaves when that holds for all
+        const int f = threadIdx.x & 127, n = first % a.tiles_n * kLM + f;
+        const long long tt = (long long)(first / a.tiles_n) * kTT + rank * per;
+        if (got && n < a.l.N) {
+            const float b0 = a.l.bias ? __ldg(a.l.bias + n) : 0.0f;
+            const float b1 = kGated && a.l.bias ? __ldg(a.l.bias + a.l.N + n) : 0.0f;
+            const int have = (int)min((long long)per, a.l.T - tt);   // tokens of the share that exist
+            const float* mine = own + rank * per * kLM + f;
+            if (per >= 8) {
+                for (int j = 8 * (threadIdx.x >> 7); j < have; j += 8 * (kThreads / 128))
+                    join_slices<kOutF32, kGated, 8>(a.l, mine + j * kLM, kTT * kLM, inbound + j * kLM + f, per * kLM, S, rank,
+                                                    tt + j, n, b0, b1);
+            } else if (threadIdx.x < 128 && have > 0) {
+                join_slices<kOutF32, kGated, 4>(a.l, mine, kTT * kLM, inbound + f, per * kLM, S, rank, tt, n, b0, b1);
+            }
+        }
+        __syncwarp();
+        cluster_wait();
+    }
     if (*abort) {   // unwinding: let copies and products in flight land first
         const long long from = clock64();
         while (clock64() - from < 4000000) {}
     }
-    if (slices > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
-    // the cluster's CTAs share out the tile's rows; each sums the slices' partial sums in order
-    {
-        const int rows = kLM / slices;
-        constexpr int kQuads = kFeat / 4;
-        for (int i = threadIdx.x; i < rows * kQuads; i += kTcThreads) {
-            const int r = rank * rows + i / kQuads, c = 4 * (i % kQuads);
-            const long long t = (long long)m * kLM + r;
-            const int nn = n * kFeat + c;
-            if (t >= a.l.T || nn >= a.l.N) continue;
-            const float* mine = part + r * kPitch + c;
-            float z[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int q = 0; q < slices; ++q) {
-                const uint32_t at = slices > 1 ? map_to_rank(mine, q) : smem_u32(mine);
-                const float4 p = slices > 1 ? ld_dsmem_f4(at) : *reinterpret_cast<const float4*>(mine);
-                z[0] += p.x; z[1] += p.y; z[2] += p.z; z[3] += p.w;
-                if (kGated) {
-                    const float4 v = slices > 1 ? ld_dsmem_f4(at + kFeat * 4) : *reinterpret_cast<const float4*>(mine + kFeat);
-                    u[0] += v.x; u[1] += v.y; u[2] += v.z; u[3] += v.w;
-                }
-            }
-            const int valid = min(4, a.l.N - nn);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j >= valid) break;
-                if (a.l.bias) {
-                    z[j] += __ldg(a.l.bias + nn + j);
-                    if (kGated) u[j] += __ldg(a.l.bias + a.l.N + nn + j);
-                }
-                z[j] = kGated ? z[j] * sigmoid_f32<kOutF32>(z[j]) * u[j] : apply_act<kOutF32>(a.l.act, z[j]);
-            }
-            constexpr int kSize = kOutF32 ? 4 : 2;
-            if (valid == 4 && a.y_tma && (!a.l.residual || a.r_vec)) {   // rows of whole 16 bytes: vectors
-                if (a.l.residual) {
-                    const uint8_t* p = static_cast<const uint8_t*>(a.l.residual) + (t * a.l.r_stride + nn) * kSize;
-                    if (kOutF32) {
-                        const float4 q = *reinterpret_cast<const float4*>(p);
-                        z[0] += q.x; z[1] += q.y; z[2] += q.z; z[3] += q.w;
-                    } else {
-                        const uint2 q = *reinterpret_cast<const uint2*>(p);
-                        z[0] += elem_f32<kF16>((uint16_t)(q.x & 0xffffu)); z[1] += elem_f32<kF16>((uint16_t)(q.x >> 16));
-                        z[2] += elem_f32<kF16>((uint16_t)(q.y & 0xffffu)); z[3] += elem_f32<kF16>((uint16_t)(q.y >> 16));
-                    }
-                }
-                uint8_t* p = static_cast<uint8_t*>(a.l.y) + (t * a.l.y_stride + nn) * kSize;
-                if (kOutF32) *reinterpret_cast<float4*>(p) = make_float4(z[0], z[1], z[2], z[3]);
-                else *reinterpret_cast<uint2*>(p) = make_uint2(pack2<kF16>(z[0], z[1]), pack2<kF16>(z[2], z[3]));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < valid) store_output<kF16, kOutF32>(a.l, t, nn + j, z[j]);
-            }
-        }
-    }
-    tc_fence_before();
-    if (slices > 1) {   // no CTA leaves while another may read its partial sums
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
-    }
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * kTN);
+        tmem_dealloc(tmem, kTmem);
     }
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, size_t smem, int cluster_x, cudaStream_t st, Args&&... args) {
+cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, int cluster_x, cudaStream_t st,
+                            Args&&... args) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -667,7 +846,7 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, size_t smem, in
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kTcThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
@@ -698,14 +877,14 @@ TcArgs tc_args(const LinearArgs& l) {
 
 // Clusters of two that fit the device at one time (each takes both SMs' shared memory whole).
 template <typename Kernel>
-int pair_clusters(Kernel kernel, size_t smem, int num_sms) {
+int pair_clusters(Kernel kernel, int threads, size_t smem, int num_sms) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(num_sms / 2 * 2);
-    cfg.blockDim = dim3(kTcThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -717,7 +896,8 @@ int pair_clusters(Kernel kernel, size_t smem, int num_sms) {
 template <bool kF16, bool kOutF32, bool kGated>
 cudaError_t launch_pair(const LinearArgs& l, cudaStream_t st) {
     constexpr int kTN = kOutF32 ? 128 : 256, kFeat = kGated ? kTN / 2 : kTN;
-    constexpr size_t kSmem = 1024 + kPairStages * (kLM * 128 + kTN / 2 * 128) + 2 * kStageBuf + 2 * 128 * 4 + sizeof(PairSmem);
+    constexpr int kGroups = kGated ? 2 : 4, kStages = kGroups == 2 ? 6 : 5, kThreads = tc_threads(kGroups);
+    constexpr size_t kSmem = 1024 + kStages * (kLM * 128 + kTN / 2 * 128) + kGroups * kStageBuf + 256 * 4 + sizeof(PairSmem);
     static_assert(kSmem <= 232448, "shared memory of one CTA");
     auto* kernel = linear_pair<kF16, kOutF32, kGated, kTN>;
     static std::atomic<int> clusters[64];
@@ -729,7 +909,7 @@ cudaError_t launch_pair(const LinearArgs& l, cudaStream_t st) {
     if (nc == 0) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
         if (e != cudaSuccess) return e;
-        nc = pair_clusters(kernel, kSmem, l.num_sms);
+        nc = pair_clusters(kernel, kThreads, kSmem, l.num_sms);
         if (nc <= 0) return cudaErrorNotSupported;
         clusters[dev].store(nc);
     }
@@ -740,58 +920,148 @@ cudaError_t launch_pair(const LinearArgs& l, cudaStream_t st) {
     if ((e = make_maps(l, kTN / 2, a.y_tma, &x, &w, &y)) != cudaSuccess) return e;
     const long long tiles = (long long)a.tiles_m * a.tiles_n;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_clusters(kernel, dim3(2 * (unsigned)(tiles < nc ? tiles : nc)), kSmem, 2, st, x, w, y, a);
+    return launch_clusters(kernel, dim3(2 * (unsigned)(tiles < nc ? tiles : nc)), kThreads, kSmem, 2, st, x, w, y, a);
 }
 
-template <bool kF16, bool kOutF32, bool kGated, int kTN>
-cudaError_t launch_split_tn(const LinearArgs& l, int slices, cudaStream_t st) {
-    constexpr int kFeat = kGated ? kTN / 2 : kTN, kSmem = SplitShape<kTN>::kBytes;
-    static_assert(kSmem <= 232448, "shared memory of one CTA");
-    auto* kernel = linear_split<kF16, kOutF32, kGated, kTN>;
+template <bool kOutF32, bool kGated, int kTT>
+cudaError_t launch_feat_tt(const LinearArgs& l, int slices, cudaStream_t st) {
+    constexpr int G = kGated ? 2 : 1, kBlock = G * kLM * 128 + kTT * 128, kSub = feat_sub(kBlock), kStage = kSub * kBlock, kPart = G * kTT * kLM * 4;
+    constexpr int kMost = 220 * 1024;   // the barriers are in static shared memory
+    auto* kernel = linear_feat<kOutF32, kGated, kTT>;
     static std::atomic<bool> set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!set[dev].load()) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kMost);
+        if (e == cudaSuccess && slices > 8) e = cudaErrorInvalidValue;
         if (e != cudaSuccess) return e;
         set[dev].store(true);
     }
-    const TcArgs a = tc_args(l);
+    FeatArgs a{};
+    a.l = l;
+    a.nkb = (l.K + kSub * kLK - 1) / (kSub * kLK);
+    a.tiles_n = (l.N + kLM - 1) / kLM;
+    a.tiles_t = (l.T + kTT - 1) / kTT;
+    a.slices = slices;
+    const long long tiles = (long long)a.tiles_n * a.tiles_t;
+    if (tiles > INT32_MAX / 16 || slices > a.nkb) return cudaErrorInvalidValue;
+    const int blocks_of = (a.nkb + slices - 1) / slices;
+    const long long blocks = tiles * slices > l.num_sms && slices == 1 ? l.num_sms : tiles * slices;
+    const long long work = blocks_of * ((tiles * slices + blocks - 1) / blocks);   // K blocks a CTA goes through
+    if (kTT / slices < 4 || (slices > 1 && 2 * kPart > kMost)) return cudaErrorInvalidValue;
+    const int room = kMost - (slices > 1 ? kPart : 0);
+    a.stages = room / kStage < kFeatStages ? room / kStage : kFeatStages;
+    if (work < a.stages) a.stages = (int)work;   // no more than it uses: the next kernel's CTAs may start beside
+    a.ring = a.stages * kStage;
+    if (slices > 1 && a.ring < kPart) a.ring = kPart;
+    size_t smem = (size_t)a.ring + (slices > 1 ? kPart : 0);
+    // CTAs on one SM have to get their TMEM columns without waiting for each other (those of one cluster wait at
+    // its barriers): no more of them than 512 / kTmem fit in the 228 KB
+    constexpr int kAcc = G * kTT, kCols = 2 * kAcc <= 512 ? 2 * kAcc : kAcc, kFit = 512 / (kCols < 32 ? 32 : kCols);
+    constexpr size_t kLeast = 228 * 1024 / (kFit + 1);
+    if (smem < kLeast) smem = kLeast;
     CUtensorMap x{}, w{};
-    if ((e = make_maps(l, kGated ? kTN / 2 : kTN, false, &x, &w, nullptr)) != cudaSuccess) return e;
-    const dim3 grid(slices, (l.N + kFeat - 1) / kFeat, (l.T + kLM - 1) / kLM);
-    return launch_clusters(kernel, grid, kSmem, slices, st, x, w, a);
+    e = make_tmap_bf16_2d(&x, l.x, l.T, l.K, l.x_stride * 2, kLK, kTT);
+    if (e == cudaSuccess) e = make_tmap_bf16_2d(&w, l.w, l.rows, l.K, l.w_stride * 2, kLK, kLM);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(kernel, dim3((unsigned)blocks), tc_threads(feat_groups(kTT)), 1024 + smem, slices, st, x, w, a);
 }
 
-// Which kernel.  linear_split while its 64-feature tiles are few; each tile gets as many slices of K (a
-// power of two, at least four blocks each) as there are SMs to take them.
-template <bool kF16, bool kOutF32, bool kGated>
-cudaError_t launch_tc(const LinearArgs& l, cudaStream_t st) {
-    const long long tm = (l.T + kLM - 1) / kLM;
-    const long long t64 = tm * ((l.rows + 63) / 64), t128 = tm * ((l.rows + 127) / 128);
-    const int nkb = (l.K + kLK - 1) / kLK;
-    if (t128 <= l.num_sms) {
-        const bool wide = t64 > l.num_sms;
-        const long long tiles = wide ? t128 : t64;
-        int s = 1;
-        while (s < 8 && tiles * s * 2 <= l.num_sms && nkb >= 8 * s) s *= 2;
-        return wide ? launch_split_tn<kF16, kOutF32, kGated, 128>(l, s, st) : launch_split_tn<kF16, kOutF32, kGated, 64>(l, s, st);
+template <bool kOutF32, bool kGated>
+cudaError_t launch_feat(const LinearArgs& l, int tt, int slices, cudaStream_t st) {
+    switch (tt) {
+        case 16: return launch_feat_tt<kOutF32, kGated, 16>(l, slices, st);
+        case 32: return launch_feat_tt<kOutF32, kGated, 32>(l, slices, st);
+        case 64: return launch_feat_tt<kOutF32, kGated, 64>(l, slices, st);
+        case 128:
+            if constexpr (!(kOutF32 && kGated)) return launch_feat_tt<kOutF32, kGated, 128>(l, slices, st);
+            break;
+        case 256:
+            if constexpr (!kOutF32 && !kGated) return launch_feat_tt<kOutF32, kGated, 256>(l, slices, st);
+            break;
     }
-    return launch_pair<kF16, kOutF32, kGated>(l, st);
+    return cudaErrorInvalidValue;
+}
+
+// Which kernel and tile: the least of an estimate in microseconds, fitted to runs of every form on products of
+// 1..4096 tokens (it is within about a tenth of them).  Per tile a CTA, or a pair, needs the longer of its K loop
+// and its epilogue, as the two overlap; the launch, the last epilogue and joining slices come once.
+struct Plan {
+    bool pair;
+    int tt, slices;
+    double us;
+};
+
+// Clusters of a size that run at a time with one CTA to an SM, as the device reports it: 152 SMs hold 76 of 2, 36
+// of 4 and 15 of 8.
+int clusters_at_once(int size, int num_sms) {
+    return size == 1 ? num_sms : size == 2 ? num_sms / 2 : size == 4 ? num_sms * 36 / 152 : num_sms * 15 / 152;
+}
+
+Plan plan_tc(const LinearArgs& l) {
+    const bool gated = l.act == MOE_ACT_SWIGLU, costly = l.act != MOE_ACT_NONE && l.act != MOE_ACT_RELU;
+    const int nkb = (l.K + kLK - 1) / kLK, G = gated ? 2 : 1;
+    const double kLaunch = 1.4, kL2 = 17e6;                        // us; bytes a us that L2 gives all SMs together
+    const double kLoop[5] = {0.142, 0.155, 0.19, 0.215, 0.30};     // us of 64 columns for 16, 32, .. 256 tokens
+    const double kLoopGated[4] = {0.26, 0.28, 0.34, 0.41};
+    Plan best{false, 0, 1, 1e300};
+    const auto consider = [&](bool pair, int tt, int s, int sub, double tiles, double slots, double block_us,
+                              double block_bytes, double epilogue, double once) {
+        const double waves = s > 1 ? 1 : (double)(((long long)tiles + (long long)slots - 1) / (long long)slots);
+        const double busy = tiles * s < slots ? tiles * s : slots, shared = block_bytes * busy / kL2;
+        const int stages = (nkb + sub - 1) / sub;
+        const double loop = (double)((stages + s - 1) / s) * sub * (block_us > shared ? block_us : shared);
+        const double us = kLaunch + once + waves * (loop > epilogue ? loop : epilogue) + epilogue;
+        if (us < best.us) best = Plan{pair, tt, s, us};
+    };
+    const int most = l.out_f32 ? (gated ? 64 : 128) : (gated ? 128 : 256);
+    for (int tt = 16, i = 0; tt <= most; tt *= 2, ++i) {
+        const double tiles = (double)((l.N + kLM - 1) / kLM) * ((l.T + tt - 1) / tt);
+        const int bytes = (G * kLM + tt) * 128, sub = feat_sub(bytes);
+        const double epilogue = (costly ? 0.016 : 0.010) * tt * (gated ? 1.3 : 1.0);
+        for (int s = 1; s <= 8; s *= 2) {
+            if (s > 1 && (tiles > clusters_at_once(s, l.num_sms) || (nkb + sub - 1) / sub < s || tt / s < 4 || G * tt > 128))
+                break;
+            consider(false, tt, s, sub, tiles, l.num_sms, gated ? kLoopGated[i] : kLoop[i], bytes, epilogue,
+                     s > 1 ? 1.7 + 0.010 * tt * G : 0.0);
+        }
+        if (tt >= l.T) break;
+    }
+    if (l.T > kLM) {
+        const int tn = l.out_f32 ? 128 : 256;
+        const double tiles = (double)((l.T + 2 * kLM - 1) / (2 * kLM)) * ((l.rows + tn - 1) / tn);
+        // rows of y or the residual at other than multiples of 16 bytes: element stores and loads
+        const int size = l.out_f32 ? 4 : 2;
+        const double slow = (l.residual && l.r_stride * size % 16 ? 20.0 : 0.0) + (l.y_stride * size % 16 ? 2.0 : 0.0);
+        consider(true, 0, 1, 1, tiles, l.num_sms / 2, tn == 256 ? 0.32 : 0.25, (2 * kLM + tn) * 128,
+                 (costly ? 4.5 : 3.0) + slow, 0.0);
+    }
+    return best;
+}
+
+template <bool kOutF32, bool kGated>
+cudaError_t launch_tc(const LinearArgs& l, cudaStream_t st) {
+    const Plan p = plan_tc(l);
+    if (!p.pair) return launch_feat<kOutF32, kGated>(l, p.tt, p.slices, st);
+    return l.f16 ? launch_pair<true, kOutF32, kGated>(l, st) : launch_pair<false, kOutF32, kGated>(l, st);
 }
 
 }  // namespace
 
+// For the choice against linear_rows, which the workspace's size rests on: on 152 SMs whatever the device at hand,
+// so that the size is the same where it is asked for and where it is used.
+double linear_tc_us(const LinearArgs& l) {
+    LinearArgs m = l;
+    m.num_sms = 152;
+    return plan_tc(m).us;
+}
+
 cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
     const bool g = l.act == MOE_ACT_SWIGLU;
-    if (l.f16) {
-        if (l.out_f32) return g ? launch_tc<true, true, true>(l, st) : launch_tc<true, true, false>(l, st);
-        return g ? launch_tc<true, false, true>(l, st) : launch_tc<true, false, false>(l, st);
-    }
-    if (l.out_f32) return g ? launch_tc<false, true, true>(l, st) : launch_tc<false, true, false>(l, st);
-    return g ? launch_tc<false, false, true>(l, st) : launch_tc<false, false, false>(l, st);
+    if (l.out_f32) return g ? launch_tc<true, true>(l, st) : launch_tc<true, false>(l, st);
+    return g ? launch_tc<false, true>(l, st) : launch_tc<false, false>(l, st);
 }
 
 }  // namespace moe

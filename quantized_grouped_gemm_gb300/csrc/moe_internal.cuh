@@ -431,6 +431,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------- misc ---------------------------------------------------
+// exp(x) = 2^t 2^r with t = x log2(e) rounded and r what the rounding left; the hardware's 2^t is good to
+// about 2^-22, and 2^r = 1 + r ln 2 to first order (|r| < 2^-16 for |x| < 100).
+__device__ __forceinline__ float exp_f32(float x) {
+    const float t = x * 1.44269504f;
+    const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504f, -t));   // log2(e) = 1.44269504 + 1.926e-8 as floats
+    float p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+    return fmaf(p * 0.693147181f, r, p);
+}
 __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -774,6 +783,7 @@ struct LinearArgs {
 };
 size_t linear_workspace(const LinearArgs& a);
 cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t st);   // linear_tc.cu; rows at multiples of 16 bytes
+double linear_tc_us(const LinearArgs& a);   // what launch_linear_tc is expected to take
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st, unsigned long long* launches);
 
 // Encodes 2-D bf16 tensor maps (host; driver entry point fetched through the runtime).

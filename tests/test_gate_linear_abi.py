@@ -93,3 +93,17 @@ def test_dispatch_refusals(lib):
     assert lib.moe_dispatch(ctypes.byref(z), None, None, None, 0, None, None) == _lib.MOE_OK
     full = _lib.moe_routing(*([256] * 8))
     assert lib.moe_dispatch(ctypes.byref(s), 256, ctypes.byref(full), 256, 1024, None, None) == WS
+
+
+def test_linear_workspace_sizes(lib):
+    """A status word; rows that start at no multiple of 16 bytes add an aligned copy of their operand."""
+    def size(**kw):
+        return lib.moe_linear_workspace_bytes(ctypes.byref(_lib.moe_linear_config(**{**LINEAR, **kw})))
+    up = lambda v: (v + 255) // 256 * 256   # noqa: E731
+    assert size() == size(T=0) == size(T=1 << 20, N=1 << 20, K=65536) == 256
+    assert size(T=500, K=1001) == 256 + up(64 * 1008 * 2) + up(500 * 1008 * 2)
+    assert size(T=500, K=1001, activation=_lib.MOE_ACT_SWIGLU) == 256 + up(128 * 1008 * 2) + up(500 * 1008 * 2)
+    assert size(T=500, K=1000, x_stride=1003) == 256 + up(500 * 1000 * 2)
+    assert size(T=500, K=1000, w_stride=1003) == 256 + up(64 * 1000 * 2)
+    assert size(T=500, K=1001, x_stride=1008, w_stride=1008) == 256
+    assert size(T=500, y_stride=67, residual_stride=65) == 256
