@@ -216,8 +216,9 @@ def gate_config(T: int, E: int = 256, k: int = 8, score: str = "softmax", dtype:
 
 def moe_gate(cfg, logits, select_bias, topk_idx, topk_w, stream=None) -> None:
     """The k experts and weights of every token, into topk_idx (int32) and topk_w (fp32) [T, k]."""
-    _check(lib().moe_gate(ctypes.byref(cfg), _p(logits), _p(select_bias), _p(topk_idx), _p(topk_w), _s(stream)),
-           "moe_gate")
+    rc = lib().moe_gate(cfg, logits.data_ptr(), _p(select_bias), topk_idx.data_ptr(), topk_w.data_ptr(), _s(stream))
+    if rc != MOE_OK:
+        raise MoEError("moe_gate", rc)
 
 
 def moe_dispatch(shp, x, routing: Routing, ws, opts=None, stream=None) -> None:
@@ -251,5 +252,7 @@ def linear_workspace(cfg, device="cuda") -> torch.Tensor:
 
 def moe_linear(cfg, x, w, bias, residual, y, ws, stream=None) -> None:
     """y = act(x w^T + bias) + residual; bias (fp32) and residual may be None, y may be residual."""
-    _check(lib().moe_linear(ctypes.byref(cfg), _p(x), _p(w), _p(bias), _p(residual), _p(y), _p(ws), ws.numel(),
-                            _s(stream)), "moe_linear")
+    rc = lib().moe_linear(cfg, x.data_ptr(), w.data_ptr(), _p(bias), _p(residual), y.data_ptr(), ws.data_ptr(),
+                          ws.numel(), _s(stream))
+    if rc != MOE_OK:
+        raise MoEError("moe_linear", rc)

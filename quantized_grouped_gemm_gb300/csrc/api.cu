@@ -505,6 +505,7 @@ static int linear_args(const moe_linear_config* c, LinearArgs* a) {
     a->r_stride = strides[2] ? strides[2] : c->N;
     a->y_stride = strides[3] ? strides[3] : c->N;
     a->num_sms = num_sms();
+    a->few = linear_takes_rows(*a);
     return MOE_OK;
 }
 

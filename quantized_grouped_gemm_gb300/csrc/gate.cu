@@ -19,7 +19,7 @@ namespace moe {
 namespace {
 
 constexpr int kGateWarps = 8;
-constexpr int kMaxCand = 128;   // candidates ranked by counting: up to 4 a lane
+constexpr int kMaxCand = 256;   // candidates kept for ranking: up to 8 a lane
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kInf = __builtin_huge_valf(), kMaxF = 3.402823466e+38f;
 
@@ -43,15 +43,23 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Scores; those below exp(kLowest), next to the smallest normal number, are 0, and so are those of -inf and NaN.
-constexpr float kLowest = -87.0f;
-__device__ __forceinline__ float sigmoid_score(float l) {
-    const float d = 1.0f + exp_f32(fminf(fmaxf(-l, -88.0f), -kLowest));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-    return l > kLowest ? r : 0.0f;
+// 2^t by the hardware, good to about 2^-22, results below 2^-126 as 0.
+__device__ __forceinline__ float exp2_f32(float t) {
+    float p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+    return p;
 }
-__device__ __forceinline__ float softmax_term(float x) { return x > kLowest ? exp_f32(x) : 0.0f; }   // x = logit - largest
+constexpr float kLog2e = 1.44269504f;
+// Logits (softmax: less the largest) from which on a score is 0, next to the smallest normal number.
+constexpr float kLowest = -87.0f;
+// Scores.  The argument's rounding, 2^-24 |x log2 e|, is a relative error of at most 1e-6 of scores down to exp(-8)
+// of the largest (a sigmoid near 1 has a (1 - s)-th of it).  -inf and NaN (fmaxf drops it) give 0.
+__device__ __forceinline__ float sigmoid_score(float l) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_f32(fmaxf(l, -__builtin_huge_valf()) * -kLog2e)));
+    return r;
+}
+__device__ __forceinline__ float softmax_term(float x) { return exp2_f32(fmaxf(x, -__builtin_huge_valf()) * kLog2e); }
 
 template <typename T> __device__ __forceinline__ float logit_f32(T v, bool f16);
 template <> __device__ __forceinline__ float logit_f32<float>(float v, bool) { return v; }
@@ -63,8 +71,14 @@ template <> __device__ __forceinline__ float logit_f32<uint16_t>(uint16_t v, boo
 template <typename T, int P, int S, GateMode kMode>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
     constexpr bool kByScore = kMode == kScores || kMode == kGroups;
-    __shared__ __align__(16) float c_v[kGateWarps][kMaxCand];   // the candidates' values,
-    __shared__ float2 c_se[kGateWarps][kMaxCand];               // scores and indices
+    constexpr int kCap = 32 * P < kMaxCand ? 32 * P : kMaxCand;
+    __shared__ __align__(16) float c_v[kGateWarps][kCap];   // the candidates' values,
+    __shared__ float2 c_se[kGateWarps][kCap];               // scores (or logits) and indices
+    // A candidate's score is kept where a lane holds few experts.  Else it is worked out again from the logit of the
+    // chosen, so that the scores need no registers after the choice values (4096 x 512, k = 10 in bf16 with bias:
+    // 5.8 against 6.9 us; one token of 256 experts 2.6 against 2.1 us, the reload's latency).  By logits the value
+    // is the score's argument.
+    constexpr bool kKeep = kByScore && P <= 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long tok = (long long)blockIdx.x * kGateWarps + warp;
     pdl_wait();
@@ -99,9 +113,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
         for (int i = 0; i < P; ++i) s[i] = i < cnt ? logit_f32<T>(row[i], a.f16) : -kInf;
     }
 
-    float inv = 1.0f;
+    float inv = 1.0f, m = 0.0f;
     if (!a.sigmoid) {
-        float m = s[0];
+        m = s[0];
 #pragma unroll
         for (int i = 1; i < P; ++i) m = fmaxf(m, s[i]);   // fmaxf drops a NaN
         m = warp_max(m);
@@ -199,7 +213,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
     }
 
     // candidates: one a lane where a lane holds one expert anyway
-    float cv = v[0], cs = s[0];
+    float cv = v[0], cs = kKeep ? s[0] : v[0];
     int ce = e0, cand = 32;
     if (P > 1) {
         float h[S];
@@ -222,25 +236,33 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
                 if (h[q] == top) h[q] = -kInf;
         }
         bound = fmaxf(bound, -kMaxF);     // fewer than k samples: everything that can be chosen
-        const uint32_t below = (1u << lane) - 1u;
         c_v[warp][lane] = -kInf;          // ranks are counted in fours
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) mine += v[i] >= bound;
+        int at = mine;   // inclusive sum over the lanes, so candidates are kept in the order of their indices
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int other = __shfl_up_sync(kAll, at, o);
+            if (lane >= o) at += other;
+        }
+        cand = __shfl_sync(kAll, at, 31);
+        at -= mine;
         __syncwarp();
-        cand = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const bool in = v[i] >= bound;
-            const uint32_t mask = __ballot_sync(kAll, in);
-            const int at = cand + __popc(mask & below);
-            cand += __popc(mask);
-            if (in && at < kMaxCand) {
-                c_v[warp][at] = v[i];
-                c_se[warp][at] = make_float2(s[i], __int_as_float(e0 + i));
+            if (v[i] >= bound) {
+                if (32 * P <= kCap || at < kCap) {
+                    c_v[warp][at] = v[i];
+                    c_se[warp][at] = make_float2(kKeep ? s[i] : v[i], __int_as_float(e0 + i));
+                }
+                ++at;
             }
         }
         __syncwarp();
         if (cand <= 32) {
+            const float2 se = c_se[warp][lane < cand ? lane : 0];
             cv = c_v[warp][lane];
-            const float2 se = c_se[warp][lane & (cand > lane ? 31 : 0)];
             cs = se.x;
             ce = __float_as_int(se.y);
         }
@@ -259,36 +281,33 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
         if (done && lane < cand && rank < a.k) slot = rank;
     }
     if (!done && cand <= 32) {
-        for (int j = 0; j < a.k; ++j) {
+        for (int j = 0; j < a.k; ++j) {   // candidates are in index order: the lowest lane of the equals
             const float top = warp_max(cv);
-            const uint32_t low = __reduce_min_sync(kAll, cv == top ? (uint32_t)ce : kAll);
-            if (cv == top && (uint32_t)ce == low) {
+            if (lane == __ffs(__ballot_sync(kAll, cv == top)) - 1) {
                 slot = j;
                 cv = -kInf;
             }
         }
-    } else if (!done && cand <= kMaxCand) {
-        float qv[kMaxCand / 32];
+    } else if (!done && cand <= kCap) {
+        float qv[kCap / 32];
 #pragma unroll
-        for (int q = 0; q < kMaxCand / 32; ++q) qv[q] = lane + 32 * q < cand ? c_v[warp][lane + 32 * q] : -kInf;
+        for (int q = 0; q < kCap / 32; ++q) qv[q] = lane + 32 * q < cand ? c_v[warp][lane + 32 * q] : -kInf;
         for (int j = 0; j < a.k; ++j) {
             float best = qv[0];
 #pragma unroll
-            for (int q = 1; q < kMaxCand / 32; ++q) best = fmaxf(best, qv[q]);
+            for (int q = 1; q < kCap / 32; ++q) best = fmaxf(best, qv[q]);
             const float top = warp_max(best);
-            uint32_t low = kAll;   // lowest index among the equals, with its place in the buffer
+            uint32_t at = kAll;   // the first of the equals
 #pragma unroll
-            for (int q = 0; q < kMaxCand / 32; ++q)
-                if (qv[q] == top)
-                    low = min(low, ((uint32_t)__float_as_int(c_se[warp][lane + 32 * q].y) << 8) | (uint32_t)(lane + 32 * q));
-            low = __reduce_min_sync(kAll, low);
-            const int at = low & 0xff;
+            for (int q = kCap / 32 - 1; q >= 0; --q)
+                if (qv[q] == top) at = lane + 32 * q;
+            at = __reduce_min_sync(kAll, at);
 #pragma unroll
-            for (int q = 0; q < kMaxCand / 32; ++q)
-                if (at == lane + 32 * q) qv[q] = -kInf;
+            for (int q = 0; q < kCap / 32; ++q)
+                if ((int)at == lane + 32 * q) qv[q] = -kInf;
             if (lane == j) {
                 slot = j;
-                ce = low >> 8;
+                ce = __float_as_int(c_se[warp][at].y);
                 cs = c_se[warp][at].x;
             }
         }
@@ -309,7 +328,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
                         found = true;
                         v[i] = -kInf;
                         e = e0 + i;
-                        sc = s[i];
+                        sc = kKeep ? s[i] : top;
                     }
             }
             e = __shfl_sync(kAll, e, from);
@@ -323,15 +342,23 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
     }
 
     float w = cs;
-    if (!kByScore) w = a.sigmoid ? sigmoid_score(cs) : softmax_term(cs) * inv;
+    if (!kKeep) {
+        if (kByScore && slot >= 0) {
+            const float l = logit_f32<T>(static_cast<const T*>(a.logits)[tok * a.stride + ce], a.f16);
+            cs = fminf(fmaxf(l, -kInf), kMaxF) - m;
+        }
+        w = cs > kLowest ? (a.sigmoid ? sigmoid_score(cs) : softmax_term(cs) * inv) : 0.0f;
+    }
     if (slot < 0) w = 0.0f;
     if (a.renormalise) {
         const float z = warp_sum(w);
-        w = z > 0.0f ? w / z : 0.0f;
+        w *= z > 0.0f ? __fdividef(a.scale, z) : 0.0f;
+    } else {
+        w *= a.scale;
     }
     if (slot >= 0) {
         a.topk_idx[tok * a.k + slot] = ce;
-        a.topk_w[tok * a.k + slot] = w * a.scale;
+        a.topk_w[tok * a.k + slot] = w;
     }
 }
 
@@ -347,14 +374,14 @@ cudaError_t launch_ps(const GateArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
 }
 
-// Samples: one a lane while k is at most two fifths of the lanes that can hold a chosen expert (about 1.3 k
-// candidates then), else four.
+// Samples: one a lane while k is at most 9/16 of the lanes that can hold a chosen expert (about 1.4 k candidates
+// then, 25 for k = 18 of 256), else four, whose rounds cost four times as much.
 template <typename T, int P>
 cudaError_t launch_p(GateArgs a, cudaStream_t st) {
     a.full = a.per == P << a.lane_shift && a.groups << a.lane_shift == 32;
     if constexpr (P >= 8) {
         const int lanes = a.groups > 1 ? a.group_topk << a.lane_shift : 32;
-        if (5 * a.k > 2 * lanes) return launch_ps<T, P, 4>(a, st);
+        if (16 * a.k > 9 * lanes) return launch_ps<T, P, 4>(a, st);
     }
     return launch_ps<T, P, 1>(a, st);
 }

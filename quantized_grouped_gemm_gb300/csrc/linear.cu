@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(256) realign_rows(Realign r0, Realign r1, int 
 // Whether linear_rows does it: few tokens, and not longer than the tensor-core kernels would take.  Its time,
 // fitted like theirs: an iteration of its eight warps covers 1024 columns of K and is a load's latency; large
 // weights stream from HBM, which the tensor-core kernels do at the full rate.
-static bool takes_rows(const LinearArgs& a) {
+bool linear_takes_rows(const LinearArgs& a) {
     if (a.T > kFewTokens) return false;
     const double bytes = 2.0 * a.rows * a.K, iterations = (a.K + 1023) / 1024;
     const bool vec = straight(a.w_stride) && straight(a.x_stride);
@@ -186,7 +186,7 @@ static bool takes_rows(const LinearArgs& a) {
 
 size_t linear_workspace(const LinearArgs& a) {
     size_t n = 256;
-    if (!takes_rows(a)) {
+    if (!a.few) {
         if (!straight(a.w_stride)) n += align_up((size_t)a.rows * padded(a.K) * 2, 256);
         if (!straight(a.x_stride)) n += align_up((size_t)a.T * padded(a.K) * 2, 256);
     }
@@ -196,7 +196,7 @@ size_t linear_workspace(const LinearArgs& a) {
 cudaError_t launch_linear(const LinearArgs& args, cudaStream_t st, unsigned long long* launches) {
     LinearArgs a = args;
     *launches += 1;
-    if (takes_rows(a)) {
+    if (a.few) {
         if (a.f16) return a.out_f32 ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);
         return a.out_f32 ? launch_rows<false, true>(a, st) : launch_rows<false, false>(a, st);
     }

@@ -772,6 +772,7 @@ struct LinearArgs {
     int T, N, K, rows;
     int act;
     bool f16, out_f32;
+    bool few;                  // linear_rows does it
     const void* x;
     const void* w;
     const float* bias;
@@ -781,6 +782,7 @@ struct LinearArgs {
     uint8_t* ws;
     int num_sms;
 };
+bool linear_takes_rows(const LinearArgs& a);   // by sizes and strides
 size_t linear_workspace(const LinearArgs& a);
 cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t st);   // linear_tc.cu; rows at multiples of 16 bytes
 double linear_tc_us(const LinearArgs& a);   // what launch_linear_tc is expected to take
