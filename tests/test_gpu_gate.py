@@ -276,3 +276,30 @@ def test_dispatch_flags_an_expert_out_of_range(T):
     assert int(rt.counts.sum()) == 8 * T - 2
     pos = rt.pos.cpu().numpy()
     assert pos.min() >= 0 and pos.max() < 8 * T
+
+
+@pytest.mark.parametrize("T", [1, 100])
+def test_the_example_layer(T):
+    """examples/gated_layer.py: projections, gate, dispatch and experts of one layer against their formulas."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "gated_layer.py")
+    spec = importlib.util.spec_from_file_location("gated_layer", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    layer = ex.GatedLayer(T, d=512, I=128, attention=384, vocab=1000)
+    a = torch.randn(T, 384, device="cuda").bfloat16()
+    r = torch.randn(T, 512, device="cuda").bfloat16()
+    for _ in range(2):
+        y, nxt = layer(a, r)
+    layer.check_status()
+    h = a.double() @ layer.w_out.double().t() + r.double()
+    assert ((layer.hidden.double() - h).abs() <= 2.0 ** -8 * h.abs() + 1e-4).all()
+    lg = layer.hidden.double() @ layer.w_router.double().t()
+    assert ((layer.logits.double() - lg).norm() / lg.norm()).item() <= 1e-6
+    ri, rw, clear = reference(layer.logits.cpu().numpy(), layer.balance.cpu().numpy(), 256, 8, "sigmoid", 8, 4, "top2",
+                              True, 2.5)
+    assert np.array_equal(layer.routing.topk_idx.cpu().numpy()[clear], ri[clear])
+    assert ex.compare_with_oracle(layer, list(range(min(T, 8)))) <= 5e-3
+    z = layer.y[-nxt.shape[0]:].double() @ layer.w_head.double().t()
+    assert ((nxt.double() - z).norm() / z.norm()).item() <= 1e-6
