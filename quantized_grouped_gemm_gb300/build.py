@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
-SOURCES = ["api.cu", "route.cu", "ffn.cu", "decode.cu", "decode_fused.cu", "pack.cu", "static_scratch.cu", "gate.cu", "linear.cu", "linear_tc.cu"]
+SOURCES = ["api.cu", "route.cu", "ffn.cu", "decode.cu", "decode_fused.cu", "pack.cu", "static_scratch.cu", "gate.cu", "linear.cu", "linear_tc_bf16.cu",
+           "linear_tc_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,6 +37,7 @@ def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
     deps = [src, os.path.join(CSRC, "moe_internal.cuh"), os.path.join(CSRC, "linear_common.cuh"),
+            os.path.join(CSRC, "linear_tc.cuh"),
             os.path.join(ROOT, "include", "moe.h")]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 

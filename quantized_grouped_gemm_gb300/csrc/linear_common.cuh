@@ -9,6 +9,25 @@
 
 namespace moe {
 
+constexpr int kLK = 64;                 // columns of K per block: one 128-byte swizzle row
+constexpr int kLM = 128;                // M of a CTA: token rows (linear_pair) or weight rows (linear_feat)
+// Blocks of 64 columns to a stage of the ring.  Waiting for a stage, issuing its products and releasing it cost
+// the issuer and the producer about 0.1 us whatever its size, so small blocks share a stage (one weight tile of
+// 2048 columns: 8.7 us with one block of 16 tokens to a stage, 6.9 with two, 6.1 with four; of 128 tokens 10.6
+// and 9.3 with two).
+__host__ __device__ constexpr int feat_sub(int block) { return block <= 20480 ? 4 : block <= 36864 ? 2 : 1; }
+
+// How the tensor cores do a product (linear.cu): by linear_pair, or by linear_feat with tt tokens to a tile and K in
+// slices; us: the time expected.
+struct LinearPlan {
+    bool pair;
+    int tt, slices;
+    double us;
+};
+LinearPlan linear_plan(const LinearArgs& l);
+cudaError_t launch_linear_tc_bf16(const LinearArgs& l, cudaStream_t st);   // rows at multiples of 16 bytes
+cudaError_t launch_linear_tc_f16(const LinearArgs& l, cudaStream_t st);
+
 #ifdef __CUDACC__
 
 // act(z) in fp32.  kExact (fp32 outputs): the exponential is good to a few 2^-23.  Else the result is rounded

@@ -1,4 +1,4 @@
-// linear_tc.cu -- moe_linear on the 5th-generation tensor cores (more than a few tokens).
+// linear_tc.cuh -- moe_linear on the 5th-generation tensor cores (more than a few tokens).
 //
 // Operands are K-major and come in by TMA as 64-column blocks with the 128-byte swizzle (TMA fills what lies
 // beyond T, N or K with zeros); the fp32 accumulators are in TMEM.
@@ -24,8 +24,6 @@
 namespace moe {
 namespace {
 
-constexpr int kLK = 64;                 // columns of K per block: one 128-byte swizzle row
-constexpr int kLM = 128;                // token rows a CTA holds
 constexpr int kChunk = 8;               // blocks summed in the accumulator for fp32 outputs
 // Threads: four warps (producer, issuer, TMEM, spare) and `groups` warpgroups of the epilogue, each with its share of
 // a tile's columns.  Four groups where the tile is wide: short K loops leave the time to the epilogue.
@@ -223,25 +221,35 @@ using OutElem = typename std::conditional<kOutF32, float, uint16_t>::type;
 // The residual of one feature n of kCnt consecutive tokens from t0, as stored (0 beyond the last token).
 template <bool kOutF32, int kCnt>
 __device__ __forceinline__ void load_residual(const LinearArgs& l, long long t0, int n, OutElem<kOutF32> (&r)[kCnt]) {
-    const long long left = l.T - t0;
-    const int cnt = n < l.N && left > 0 ? (int)min((long long)kCnt, left) : 0;
-    const OutElem<kOutF32>* p = static_cast<const OutElem<kOutF32>*>(l.residual) + t0 * l.r_stride + n;
+    using Elem = OutElem<kOutF32>;
+    const char* row = static_cast<const char*>(l.residual) + t0 * l.r_stride * (long long)sizeof(Elem);   // uniform
+    const uint32_t off = n * (uint32_t)sizeof(Elem);
+    const bool in = n < l.N;
+    if (t0 + kCnt <= l.T) {
 #pragma unroll
-    for (int j = 0; j < kCnt; ++j) {
-        r[j] = 0;
-        if (j < cnt) r[j] = *p;
-        p += l.r_stride;
+        for (int j = 0; j < kCnt; ++j) {
+            r[j] = in ? *reinterpret_cast<const Elem*>(row + off) : (Elem)0;
+            row += l.r_stride * (long long)sizeof(Elem);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kCnt; ++j) {
+            r[j] = in && t0 + j < l.T ? *reinterpret_cast<const Elem*>(row + off) : (Elem)0;
+            row += l.r_stride * (long long)sizeof(Elem);
+        }
     }
 }
 
-// Bias, activation, residual (r, as stored) and store of one feature n of kCnt consecutive tokens from t0 (z: products,
-// u: the up projection's).
-template <bool kOutF32, bool kGated, int kCnt, int kUp>
+// Bias, activation, residual (r, as stored) and store of one feature n < N of kCnt consecutive tokens from t0 (z:
+// products, u: the up projection's).
+template <bool kF16, bool kOutF32, bool kGated, int kCnt, int kUp>
 __device__ __forceinline__ void finish_column(const LinearArgs& l, long long t0, int n, float b0, float b1,
                                               float (&z)[kCnt], const float (&u)[kUp], const OutElem<kOutF32> (&r)[kCnt]) {
-    const int cnt = (int)min((long long)kCnt, l.T - t0);
+    using Elem = OutElem<kOutF32>;
+    if (l.bias) {
 #pragma unroll
-    for (int j = 0; j < kCnt; ++j) z[j] += b0;
+        for (int j = 0; j < kCnt; ++j) z[j] += b0;
+    }
     if (kGated) {
 #pragma unroll
         for (int j = 0; j < kCnt; ++j) z[j] = z[j] * sigmoid_f32<kOutF32>(z[j]) * (u[kGated ? j : 0] + b1);
@@ -252,17 +260,23 @@ __device__ __forceinline__ void finish_column(const LinearArgs& l, long long t0,
 #pragma unroll
         for (int j = 0; j < kCnt; ++j) {
             if constexpr (kOutF32) z[j] += r[j];
-            else z[j] += l.f16 ? elem_f32<true>(r[j]) : elem_f32<false>(r[j]);
+            else z[j] += elem_f32<kF16>(r[j]);
         }
     }
-    OutElem<kOutF32>* y = static_cast<OutElem<kOutF32>*>(l.y) + t0 * l.y_stride + n;
+    char* row = static_cast<char*>(l.y) + t0 * l.y_stride * (long long)sizeof(Elem);   // uniform
+    const uint32_t off = n * (uint32_t)sizeof(Elem);
+    const auto put = [&](int j) {
+        if constexpr (kOutF32) *reinterpret_cast<float*>(row + off) = z[j];
+        else *reinterpret_cast<uint16_t*>(row + off) = elem_from_f32<kF16>(z[j]);
+        row += l.y_stride * (long long)sizeof(Elem);
+    };
+    if (t0 + kCnt <= l.T) {
 #pragma unroll
-    for (int j = 0; j < kCnt; ++j) {
-        if (j < cnt) {
-            if constexpr (kOutF32) *y = z[j];
-            else *y = l.f16 ? elem_from_f32<true>(z[j]) : elem_from_f32<false>(z[j]);
-        }
-        y += l.y_stride;
+        for (int j = 0; j < kCnt; ++j) put(j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kCnt; ++j)
+            if (t0 + j < l.T) put(j);
     }
 }
 
@@ -550,7 +564,7 @@ __device__ __forceinline__ void bulk_s2s(uint32_t dst, const void* src, uint32_t
 
 // Sums the slices' partial sums of kCnt tokens of feature f, in slice order, and finishes them.  own: this CTA's
 // sums of these tokens; in: the same of slice 0 in its inbound buffer; rows of 128 features.
-template <bool kOutF32, bool kGated, int kCnt>
+template <bool kF16, bool kOutF32, bool kGated, int kCnt>
 __device__ __forceinline__ void join_slices(const LinearArgs& l, const float* own, int own_g, const float* in, int in_g,
                                             int slices, int rank, long long t, int n, float b0, float b1) {
     float v[kCnt] = {}, up[kCnt] = {};
@@ -565,14 +579,8 @@ __device__ __forceinline__ void join_slices(const LinearArgs& l, const float* ow
             if (kGated) up[u] += p[gg + u * kLM];
         }
     }
-    finish_column<kOutF32, kGated, kCnt>(l, t, n, b0, b1, v, up, res);
+    finish_column<kF16, kOutF32, kGated, kCnt>(l, t, n, b0, b1, v, up, res);
 }
-
-// Blocks of 64 columns to a stage of the ring.  Waiting for a stage, issuing its products and releasing it cost
-// the issuer and the producer about 0.1 us whatever its size, so small blocks share a stage (one weight tile of
-// 2048 columns: 8.7 us with one block of 16 tokens to a stage, 6.9 with two, 6.1 with four; of 128 tokens 10.6
-// and 9.3 with two).
-__host__ __device__ constexpr int feat_sub(int block) { return block <= 20480 ? 4 : block <= 36864 ? 2 : 1; }
 
 __host__ __device__ constexpr int feat_groups(int tokens) { return tokens >= 64 ? 4 : 2; }   // warpgroups of the epilogue
 
@@ -586,7 +594,7 @@ struct FeatArgs {
 // token at once whatever the alignment of y, and a tile costs as many token columns as there are tokens.
 // kTT: tokens of a tile.  kGated: a tile has 128 gate rows and the 128 up rows of the same features, each with
 // its own accumulator.
-template <bool kOutF32, bool kGated, int kTT>
+template <bool kF16, bool kOutF32, bool kGated, int kTT>
 __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
     linear_feat(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, FeatArgs a) {
     constexpr int G = kGated ? 2 : 1;
@@ -601,7 +609,7 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     __shared__ FeatSmem sh;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (known to be uniform)
     const int S = a.slices, rank = S > 1 ? (int)cluster_ctarank() : 0, stages = a.stages;
     // slices > 1: this CTA's partial sums [G][kTT][128 features] take the ring's place, those of the other slices
     // for its share of the tokens arrive in [slice][G][per][128]
@@ -678,7 +686,7 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
         }
         if (!ok && lane == 0) { *abort = 1; set_status(status, MOE_STATUS_TIMEOUT); }
     } else if (warp == 1) {
-        const uint32_t idesc = idesc_f16kind(a.l.f16, kLM, kTT);
+        const uint32_t idesc = idesc_f16kind(kF16, kLM, kTT);
         int s = 0, buf = 0;
         uint32_t ph = 0, eph = 1;
         bool ok = true;
@@ -779,7 +787,7 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
                                                          ni % a.tiles_n * kLM + r, res);
                         }
                     }
-                    if (n < a.l.N) finish_column<kOutF32, kGated, kBlk>(a.l, t0 + j, n, b0, b1, v, up, now);
+                    if (n < a.l.N) finish_column<kF16, kOutF32, kGated, kBlk>(a.l, t0 + j, n, b0, b1, v, up, now);
                 }
             }
             tc_fence_before();
@@ -815,10 +823,10 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
             const float* mine = own + rank * per * kLM + f;
             if (per >= 8) {
                 for (int j = 8 * (threadIdx.x >> 7); j < have; j += 8 * (kThreads / 128))
-                    join_slices<kOutF32, kGated, 8>(a.l, mine + j * kLM, kTT * kLM, inbound + j * kLM + f, per * kLM, S, rank,
+                    join_slices<kF16, kOutF32, kGated, 8>(a.l, mine + j * kLM, kTT * kLM, inbound + j * kLM + f, per * kLM, S, rank,
                                                     tt + j, n, b0, b1);
             } else if (threadIdx.x < 128 && have > 0) {
-                join_slices<kOutF32, kGated, 4>(a.l, mine, kTT * kLM, inbound + f, per * kLM, S, rank, tt, n, b0, b1);
+                join_slices<kF16, kOutF32, kGated, 4>(a.l, mine, kTT * kLM, inbound + f, per * kLM, S, rank, tt, n, b0, b1);
             }
         }
         __syncwarp();
@@ -923,11 +931,11 @@ cudaError_t launch_pair(const LinearArgs& l, cudaStream_t st) {
     return launch_clusters(kernel, dim3(2 * (unsigned)(tiles < nc ? tiles : nc)), kThreads, kSmem, 2, st, x, w, y, a);
 }
 
-template <bool kOutF32, bool kGated, int kTT>
+template <bool kF16, bool kOutF32, bool kGated, int kTT>
 cudaError_t launch_feat_tt(const LinearArgs& l, int slices, cudaStream_t st) {
     constexpr int G = kGated ? 2 : 1, kBlock = G * kLM * 128 + kTT * 128, kSub = feat_sub(kBlock), kStage = kSub * kBlock, kPart = G * kTT * kLM * 4;
     constexpr int kMost = 220 * 1024;   // the barriers are in static shared memory
-    auto* kernel = linear_feat<kOutF32, kGated, kTT>;
+    auto* kernel = linear_feat<kF16, kOutF32, kGated, kTT>;
     static std::atomic<bool> set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -969,99 +977,34 @@ cudaError_t launch_feat_tt(const LinearArgs& l, int slices, cudaStream_t st) {
     return launch_clusters(kernel, dim3((unsigned)blocks), tc_threads(feat_groups(kTT)), 1024 + smem, slices, st, x, w, a);
 }
 
-template <bool kOutF32, bool kGated>
+template <bool kF16, bool kOutF32, bool kGated>
 cudaError_t launch_feat(const LinearArgs& l, int tt, int slices, cudaStream_t st) {
     switch (tt) {
-        case 16: return launch_feat_tt<kOutF32, kGated, 16>(l, slices, st);
-        case 32: return launch_feat_tt<kOutF32, kGated, 32>(l, slices, st);
-        case 64: return launch_feat_tt<kOutF32, kGated, 64>(l, slices, st);
+        case 16: return launch_feat_tt<kF16, kOutF32, kGated, 16>(l, slices, st);
+        case 32: return launch_feat_tt<kF16, kOutF32, kGated, 32>(l, slices, st);
+        case 64: return launch_feat_tt<kF16, kOutF32, kGated, 64>(l, slices, st);
         case 128:
-            if constexpr (!(kOutF32 && kGated)) return launch_feat_tt<kOutF32, kGated, 128>(l, slices, st);
+            if constexpr (!(kOutF32 && kGated)) return launch_feat_tt<kF16, kOutF32, kGated, 128>(l, slices, st);
             break;
         case 256:
-            if constexpr (!kOutF32 && !kGated) return launch_feat_tt<kOutF32, kGated, 256>(l, slices, st);
+            if constexpr (!kOutF32 && !kGated) return launch_feat_tt<kF16, kOutF32, kGated, 256>(l, slices, st);
             break;
     }
     return cudaErrorInvalidValue;
 }
 
-// Which kernel and tile: the least of an estimate in microseconds, fitted to runs of every form on products of
-// 1..4096 tokens (it is within about a tenth of them).  Per tile a CTA, or a pair, needs the longer of its K loop
-// and its epilogue, as the two overlap; the launch, the last epilogue and joining slices come once.
-struct Plan {
-    bool pair;
-    int tt, slices;
-    double us;
-};
-
-// Clusters of a size that run at a time with one CTA to an SM, as the device reports it: 152 SMs hold 76 of 2, 36
-// of 4 and 15 of 8.
-int clusters_at_once(int size, int num_sms) {
-    return size == 1 ? num_sms : size == 2 ? num_sms / 2 : size == 4 ? num_sms * 36 / 152 : num_sms * 15 / 152;
-}
-
-Plan plan_tc(const LinearArgs& l) {
-    const bool gated = l.act == MOE_ACT_SWIGLU, costly = l.act != MOE_ACT_NONE && l.act != MOE_ACT_RELU;
-    const int nkb = (l.K + kLK - 1) / kLK, G = gated ? 2 : 1;
-    const double kLaunch = 1.4, kL2 = 17e6;                        // us; bytes a us that L2 gives all SMs together
-    const double kLoop[5] = {0.142, 0.155, 0.19, 0.215, 0.30};     // us of 64 columns for 16, 32, .. 256 tokens
-    const double kLoopGated[4] = {0.26, 0.28, 0.34, 0.41};
-    Plan best{false, 0, 1, 1e300};
-    const auto consider = [&](bool pair, int tt, int s, int sub, double tiles, double slots, double block_us,
-                              double block_bytes, double epilogue, double once) {
-        const double waves = s > 1 ? 1 : (double)(((long long)tiles + (long long)slots - 1) / (long long)slots);
-        const double busy = tiles * s < slots ? tiles * s : slots, shared = block_bytes * busy / kL2;
-        const int stages = (nkb + sub - 1) / sub;
-        const double loop = (double)((stages + s - 1) / s) * sub * (block_us > shared ? block_us : shared);
-        const double us = kLaunch + once + waves * (loop > epilogue ? loop : epilogue) + epilogue;
-        if (us < best.us) best = Plan{pair, tt, s, us};
-    };
-    const int most = l.out_f32 ? (gated ? 64 : 128) : (gated ? 128 : 256);
-    for (int tt = 16, i = 0; tt <= most; tt *= 2, ++i) {
-        const double tiles = (double)((l.N + kLM - 1) / kLM) * ((l.T + tt - 1) / tt);
-        const int bytes = (G * kLM + tt) * 128, sub = feat_sub(bytes);
-        const double epilogue = (costly ? 0.016 : 0.010) * tt * (gated ? 1.3 : 1.0);
-        for (int s = 1; s <= 8; s *= 2) {
-            if (s > 1 && (tiles > clusters_at_once(s, l.num_sms) || (nkb + sub - 1) / sub < s || tt / s < 4 || G * tt > 128))
-                break;
-            consider(false, tt, s, sub, tiles, l.num_sms, gated ? kLoopGated[i] : kLoop[i], bytes, epilogue,
-                     s > 1 ? 1.7 + 0.010 * tt * G : 0.0);
-        }
-        if (tt >= l.T) break;
-    }
-    if (l.T > kLM) {
-        const int tn = l.out_f32 ? 128 : 256;
-        const double tiles = (double)((l.T + 2 * kLM - 1) / (2 * kLM)) * ((l.rows + tn - 1) / tn);
-        // rows of y or the residual at other than multiples of 16 bytes: element stores and loads
-        const int size = l.out_f32 ? 4 : 2;
-        const double slow = (l.residual && l.r_stride * size % 16 ? 20.0 : 0.0) + (l.y_stride * size % 16 ? 2.0 : 0.0);
-        consider(true, 0, 1, 1, tiles, l.num_sms / 2, tn == 256 ? 0.32 : 0.25, (2 * kLM + tn) * 128,
-                 (costly ? 4.5 : 3.0) + slow, 0.0);
-    }
-    return best;
-}
-
-template <bool kOutF32, bool kGated>
+template <bool kF16, bool kOutF32, bool kGated>
 cudaError_t launch_tc(const LinearArgs& l, cudaStream_t st) {
-    const Plan p = plan_tc(l);
-    if (!p.pair) return launch_feat<kOutF32, kGated>(l, p.tt, p.slices, st);
-    return l.f16 ? launch_pair<true, kOutF32, kGated>(l, st) : launch_pair<false, kOutF32, kGated>(l, st);
+    const LinearPlan p = linear_plan(l);
+    return p.pair ? launch_pair<kF16, kOutF32, kGated>(l, st) : launch_feat<kF16, kOutF32, kGated>(l, p.tt, p.slices, st);
+}
+
+template <bool kF16>
+cudaError_t launch_tc_type(const LinearArgs& l, cudaStream_t st) {
+    const bool g = l.act == MOE_ACT_SWIGLU;
+    if (l.out_f32) return g ? launch_tc<kF16, true, true>(l, st) : launch_tc<kF16, true, false>(l, st);
+    return g ? launch_tc<kF16, false, true>(l, st) : launch_tc<kF16, false, false>(l, st);
 }
 
 }  // namespace
-
-// For the choice against linear_rows, which the workspace's size rests on: on 152 SMs whatever the device at hand,
-// so that the size is the same where it is asked for and where it is used.
-double linear_tc_us(const LinearArgs& l) {
-    LinearArgs m = l;
-    m.num_sms = 152;
-    return plan_tc(m).us;
-}
-
-cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
-    const bool g = l.act == MOE_ACT_SWIGLU;
-    if (l.out_f32) return g ? launch_tc<true, true>(l, st) : launch_tc<true, false>(l, st);
-    return g ? launch_tc<false, true>(l, st) : launch_tc<false, false>(l, st);
-}
-
 }  // namespace moe

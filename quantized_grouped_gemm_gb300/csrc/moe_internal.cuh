@@ -784,8 +784,6 @@ struct LinearArgs {
 };
 bool linear_takes_rows(const LinearArgs& a);   // by sizes and strides
 size_t linear_workspace(const LinearArgs& a);
-cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t st);   // linear_tc.cu; rows at multiples of 16 bytes
-double linear_tc_us(const LinearArgs& a);   // what launch_linear_tc is expected to take
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st, unsigned long long* launches);
 
 // Encodes 2-D bf16 tensor maps (host; driver entry point fetched through the runtime).
