@@ -200,8 +200,9 @@ LinearPlan linear_plan(const LinearArgs& l) {
     for (int tt = 16, i = 0; tt <= most; tt *= 2, ++i) {
         const double tiles = (double)((l.N + kLM - 1) / kLM) * ((l.T + tt - 1) / tt);
         const int bytes = (G * kLM + tt) * 128, sub = feat_sub(bytes);
-        const double epilogue = gated ? 0.75 + 0.0145 * tt + (res ? 0.004 * tt : 0.0)
-                                      : 0.5 + 0.0068 * tt + act * (0.15 + 0.006 * tt) + (res ? 0.1 + 0.004 * tt : 0.0);
+        const double epilogue = (gated ? 0.75 + 0.0145 * tt + (res ? 0.004 * tt : 0.0)
+                                       : 0.5 + 0.0068 * tt + act * (0.15 + 0.006 * tt) + (res ? 0.1 + 0.004 * tt : 0.0)) *
+                                (l.out_f32 ? tt == 128 ? 1.5 : 1.17 : 1.0);
         for (int s = 1; s <= 8; s *= 2) {
             if (s > 1 && (tiles > clusters_at_once(s, l.num_sms) || (nkb + sub - 1) / sub < s || tt / s < 4 || G * tt > 128))
                 break;

@@ -281,16 +281,16 @@ __device__ __forceinline__ void finish_column(const LinearArgs& l, long long t0,
 }
 
 // kTN: weight rows of a tile (256, or 128 with fp32 outputs so that a thread's running sums fit its
-// registers); with kGated half of them are gate rows and half the up rows of the same features.
-template <bool kF16, bool kOutF32, bool kGated, int kTN>
-__global__ void __launch_bounds__(tc_threads(kGated ? 2 : 4), 1)
+// registers); with kGated half of them are gate rows and half the up rows of the same features.  kGroups: warpgroups of
+// the epilogue.
+template <bool kF16, bool kOutF32, bool kGated, int kTN, int kGroups>
+__global__ void __launch_bounds__(tc_threads(kGroups), 1)
     linear_pair(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_y, TcArgs a) {
     constexpr int kBRows = kTN / 2;                          // weight rows a CTA holds
     constexpr int kABytes = kLM * 128, kBBytes = kBRows * 128, kStage = kABytes + kBBytes;
     constexpr int kBufs = 512 / kTN;                         // accumulators in TMEM
     constexpr int kFeat = kGated ? kTN / 2 : kTN;            // outputs of a tile
-    constexpr int kGroups = kGated ? 2 : 4;                  // warpgroups of the epilogue
     constexpr int kHalf = kFeat / kGroups;                   // outputs a warpgroup handles
     constexpr int kPairStages = kGroups == 2 ? 6 : 5;
     constexpr int kGrp = kOutF32 ? 32 : 64;                  // outputs of one staging row (128 bytes)
@@ -901,13 +901,13 @@ int pair_clusters(Kernel kernel, int threads, size_t smem, int num_sms) {
     return n;
 }
 
-template <bool kF16, bool kOutF32, bool kGated>
+template <bool kF16, bool kOutF32, bool kGated, int kGroups>
 cudaError_t launch_pair(const LinearArgs& l, cudaStream_t st) {
     constexpr int kTN = kOutF32 ? 128 : 256, kFeat = kGated ? kTN / 2 : kTN;
-    constexpr int kGroups = kGated ? 2 : 4, kStages = kGroups == 2 ? 6 : 5, kThreads = tc_threads(kGroups);
+    constexpr int kStages = kGroups == 2 ? 6 : 5, kThreads = tc_threads(kGroups);
     constexpr size_t kSmem = 1024 + kStages * (kLM * 128 + kTN / 2 * 128) + kGroups * kStageBuf + 256 * 4 + sizeof(PairSmem);
     static_assert(kSmem <= 232448, "shared memory of one CTA");
-    auto* kernel = linear_pair<kF16, kOutF32, kGated, kTN>;
+    auto* kernel = linear_pair<kF16, kOutF32, kGated, kTN, kGroups>;
     static std::atomic<int> clusters[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -996,7 +996,12 @@ cudaError_t launch_feat(const LinearArgs& l, int tt, int slices, cudaStream_t st
 template <bool kF16, bool kOutF32, bool kGated>
 cudaError_t launch_tc(const LinearArgs& l, cudaStream_t st) {
     const LinearPlan p = linear_plan(l);
-    return p.pair ? launch_pair<kF16, kOutF32, kGated>(l, st) : launch_feat<kF16, kOutF32, kGated>(l, p.tt, p.slices, st);
+    if (!p.pair) return launch_feat<kF16, kOutF32, kGated>(l, p.tt, p.slices, st);
+    // Short K loops leave the time to the epilogue, and four warpgroups of it pay for a stage less in the ring (K = 512 with
+    // GELU: 52 against 58 us at 4096 x 8192; K = 2048: 344 against 336 us at 16384 x 8192).
+    if constexpr (!kOutF32 && !kGated)
+        if (l.K < 1024) return launch_pair<kF16, false, false, 4>(l, st);
+    return launch_pair<kF16, kOutF32, kGated, 2>(l, st);
 }
 
 template <bool kF16>
