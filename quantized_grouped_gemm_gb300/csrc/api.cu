@@ -432,7 +432,7 @@ int moe_gate(const moe_gate_config* c, const void* logits, const float* bias, in
         (c->group_score != MOE_GROUP_TOP2 && c->group_score != MOE_GROUP_MAX) || (c->renormalise != 0 && c->renormalise != 1) ||
         !std::isfinite(c->scale))
         return MOE_ERR_INVALID_ARG;
-    const int groups = c->groups == 0 ? 1 : c->groups;
+    int groups = c->groups == 0 ? 1 : c->groups;
     if (c->T > (1 << 20) || c->E > 1024 || c->k > 32 || groups > 32) return MOE_ERR_UNSUPPORTED;
     if (c->k > c->E || (c->logits_stride != 0 && c->logits_stride < c->E)) return MOE_ERR_INVALID_ARG;
     if (groups > 1) {
@@ -440,6 +440,7 @@ int moe_gate(const moe_gate_config* c, const void* logits, const float* bias, in
             c->k > c->group_topk * (c->E / groups) || (c->group_score == MOE_GROUP_TOP2 && c->E / groups < 2))
             return MOE_ERR_INVALID_ARG;
     }
+    if (c->group_topk == groups) groups = 1;   // every group is kept
     if (c->T == 0) return MOE_OK;
     const size_t size = c->logits_type == MOE_F32 ? 4 : 2;
     if (!logits || !idx || !w || !aligned(logits, size) || !aligned(idx, 4) || !aligned(w, 4) ||

@@ -8,9 +8,8 @@
 // found without sorting E values.  Each lane takes the maximum of each of S parts of its values; the k-th
 // largest of these 32 S samples is a lower bound B of the k-th largest value (k samples are >= B), so only
 // values >= B can be chosen -- about 9 of 256 for k = 8.  Those are compacted through shared memory, and each
-// finds its rank by counting the ones above it.  Ties (found by the ranks not being a permutation) and
-// tokens with more than kMaxCand candidates (ties by the hundred, as when every expert is switched off) take
-// k rounds of a warp-wide argmax instead.
+// finds its rank by counting the ones above it (and, when the ranks turn out not to be a permutation, the equal ones
+// before it).  More than 64 candidates go to gate_slow.
 #include "moe_internal.cuh"
 
 #include <cuda_fp16.h>
@@ -19,7 +18,7 @@ namespace moe {
 namespace {
 
 constexpr int kGateWarps = 8;
-constexpr int kMaxCand = 256;   // candidates kept for ranking: up to 8 a lane
+constexpr int kMaxCand = 64;   // candidates ranked by counting: up to two a lane
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kInf = __builtin_huge_valf(), kMaxF = 3.402823466e+38f;
 
@@ -67,13 +66,65 @@ template <> __device__ __forceinline__ float logit_f32<uint16_t>(uint16_t v, boo
     return f16 ? __half2float(__ushort_as_half(v)) : bf16f(v);
 }
 
+// A token whose candidates are too many to rank by counting (many equal values, as when experts are switched off): the
+// distinct values in turn, from the largest, each with all the experts that have it in index order, until k are chosen.
+// Lane j < k gets slot j's expert and score.  Not inlined: the usual path has to fit the instruction cache.
+struct Chosen {
+    int e;
+    float s;
+};
+template <typename T, int N>   // N: at least E / 32
+__device__ __noinline__ Chosen gate_slow(const GateArgs& a, long long tok, uint32_t groups_kept, float m, float inv) {
+    __shared__ uint16_t order[kGateWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T* row = static_cast<const T*>(a.logits) + tok * a.stride;
+    const auto score = [&](float x) { return a.sigmoid ? sigmoid_score(x) : softmax_term(x) * inv; };
+    const auto logit = [&](float x) { return fminf(fmaxf(x, -kInf), kMaxF) - m; };
+    float v[N];   // of experts lane, lane + 32, ..
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lane + 32 * i < a.E ? logit_f32<T>(row[lane + 32 * i], a.f16) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = lane + 32 * i;
+        float x = logit(v[i]);
+        if (a.bias) x = fmaxf(score(x) + __ldg(a.bias + min(e, a.E - 1)), -kMaxF);
+        else x = a.groups > 1 ? score(x) : fmaxf(x, kLowest);
+        v[i] = e < a.E && (a.groups == 1 || ((groups_kept >> (e / a.per)) & 1u)) ? x : -kInf;
+    }
+    float last = kInf;
+    for (int slots = 0; slots < a.k;) {   // (at least k experts can be chosen)
+        float best = -kInf;
+#pragma unroll
+        for (int i = 0; i < N; ++i) best = fmaxf(best, v[i] < last ? v[i] : -kInf);
+        last = warp_max(best);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t mask = __ballot_sync(kAll, v[i] == last);
+            if (mask) {
+                const int at = slots + __popc(mask & ((1u << lane) - 1u));
+                if (v[i] == last && at < a.k) order[warp][at] = (uint16_t)(lane + 32 * i);
+                slots += __popc(mask);
+            }
+        }
+    }
+    __syncwarp();
+    Chosen c{0, 0.0f};
+    if (lane < a.k) {
+        c.e = order[warp][lane];
+        const float x = logit(logit_f32<T>(row[c.e], a.f16));
+        c.s = x > kLowest || a.bias || a.groups > 1 ? score(x) : 0.0f;
+    }
+    return c;
+}
+
 // P: the most experts a lane holds (fewer at the end of a group); S: samples a lane gives to the bound.
 template <typename T, int P, int S, GateMode kMode>
-__global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
+__global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_constant__ GateArgs a) {
     constexpr bool kByScore = kMode == kScores || kMode == kGroups;
     constexpr int kCap = 32 * P < kMaxCand ? 32 * P : kMaxCand;
     __shared__ __align__(16) float c_v[kGateWarps][kCap];   // the candidates' values,
     __shared__ float2 c_se[kGateWarps][kCap];               // scores (or logits) and indices
+    __shared__ uint8_t c_win[kGateWarps][32];
     // A candidate's score is kept where a lane holds few experts.  Else it is worked out again from the logit of the
     // chosen, so that the scores need no registers after the choice values (4096 x 512, k = 10 in bf16 with bias:
     // 5.8 against 6.9 us; one token of 256 experts 2.6 against 2.1 us, the reload's latency).  By logits the value
@@ -86,8 +137,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
     if (tok >= a.T) return;
     // this lane's experts: e0 .. e0 + cnt - 1
     const int lpg = 1 << a.lane_shift, g = lane >> a.lane_shift, sub = lane & (lpg - 1);
-    const int e0 = g * a.per + sub * P;
-    const int cnt = a.full ? P : g < a.groups ? max(0, min(P, a.per - sub * P)) : 0;
+    const int e0 = g * a.per + sub * a.lane_experts;
+    const int cnt = a.full ? P : g < a.groups ? max(0, min(a.lane_experts, a.per - sub * a.lane_experts)) : 0;
     const T* row = static_cast<const T*>(a.logits) + tok * a.stride + e0;
 
     float s[P];   // logits (softmax: minus the largest), then with kByScore scores
@@ -195,15 +246,24 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
             v2 = fmaxf(fmaxf(v2, o2), fminf(v1, o1));
             v1 = fmaxf(v1, o1);
         }
-        // the group_topk best groups, one a round, the lowest lane (so the lowest group) first
-        float worth = g < a.groups ? fmaxf(a.group_max ? v1 : v1 + v2, -kMaxF) : -kInf;
-        bool kept = false;
+        // the group_topk best groups: those of at least the value that group_topk rounds of a maximum reach, unless ties
+        // make them more; then one group a round, the lowest lane (so the lowest group) first
+        const float worth = g < a.groups ? fmaxf(a.group_max ? v1 : v1 + v2, -kMaxF) : -kInf;
+        float left = worth, least = 0.0f;
         for (int j = 0; j < a.group_topk; ++j) {
-            const float top = warp_max(worth);
-            const int who = (__ffs(__ballot_sync(kAll, worth == top)) - 1) >> a.lane_shift;
-            if (g == who) {
-                kept = true;
-                worth = -kInf;
+            least = warp_max(left);
+            if (left == least) left = -kInf;
+        }
+        bool kept = worth >= least && g < a.groups;
+        if (__builtin_expect(__popc(__ballot_sync(kAll, kept)) != a.group_topk << a.lane_shift, 0)) {
+            kept = false;
+            left = worth;
+            for (int j = 0; j < a.group_topk; ++j) {
+                const float top = warp_max(left);
+                if (g == (__ffs(__ballot_sync(kAll, left == top)) - 1) >> a.lane_shift) {
+                    kept = true;
+                    left = -kInf;
+                }
             }
         }
         if (!kept) {
@@ -213,6 +273,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
     }
 
     // candidates: one a lane where a lane holds one expert anyway
+    bool slow = false;
     float cv = v[0], cs = kKeep ? s[0] : v[0];
     int ce = e0, cand = 32;
     if (P > 1) {
@@ -225,7 +286,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
         }
         float bound = -kMaxF;
 #pragma unroll 4
-        for (int j = 0; j < a.k; ++j) {   // equal samples leave together, which only lowers the bound
+        for (int j = 0; j < a.rounds; ++j) {   // equal samples leave together, which only lowers the bound
             float best = h[0];
 #pragma unroll
             for (int q = 1; q < S; ++q) best = fmaxf(best, h[q]);
@@ -235,7 +296,6 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
             for (int q = 0; q < S; ++q)
                 if (h[q] == top) h[q] = -kInf;
         }
-        bound = fmaxf(bound, -kMaxF);     // fewer than k samples: everything that can be chosen
         c_v[warp][lane] = -kInf;          // ranks are counted in fours
         int mine = 0;
 #pragma unroll
@@ -247,29 +307,29 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
             if (lane >= o) at += other;
         }
         cand = __shfl_sync(kAll, at, 31);
+        slow = cand > kCap;               // (a bound of -inf, when the samples ran out among equals, counts every lane's P)
         at -= mine;
         __syncwarp();
+        if (!slow) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            if (v[i] >= bound) {
-                if (32 * P <= kCap || at < kCap) {
+            for (int i = 0; i < P; ++i) {
+                if (v[i] >= bound) {
                     c_v[warp][at] = v[i];
                     c_se[warp][at] = make_float2(kKeep ? s[i] : v[i], __int_as_float(e0 + i));
+                    ++at;
                 }
-                ++at;
             }
         }
         __syncwarp();
         if (cand <= 32) {
             const float2 se = c_se[warp][lane < cand ? lane : 0];
-            cv = c_v[warp][lane];
+            cv = lane < cand ? c_v[warp][lane] : -kInf;
             cs = se.x;
             ce = __float_as_int(se.y);
         }
     }
 
     int slot = -1;   // the chosen expert of this lane, if any: slot, index, score (or logit)
-    bool done = false;
     if (P > 1 && cand <= 32) {
         int rank = 0;
         for (int j = 0; j < cand; j += 4) {
@@ -277,66 +337,54 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
             rank += (o.x > cv) + (o.y > cv) + (o.z > cv) + (o.w > cv);
         }
         // no ties: the ranks of the candidates are 0 .. cand - 1
-        done = __reduce_or_sync(kAll, lane < cand ? 1u << rank : 0u) == kAll >> (32 - cand);
-        if (done && lane < cand && rank < a.k) slot = rank;
+        if (__reduce_or_sync(kAll, lane < cand ? 1u << rank : 0u) != kAll >> (32 - cand)) {
+            rank = 0;   // ties: the candidates are in index order
+            for (int j = 0; j < cand; ++j) {
+                const float o = c_v[warp][j];
+                rank += o > cv || (o == cv && j < lane);
+            }
+        }
+        if (lane < cand && rank < a.k) slot = rank;
+    } else if (P > 1 && !slow) {
+        // two a lane; chosen when the ranks below k are all there, once each
+        if (lane < 4 && cand + lane < kCap) c_v[warp][cand + lane] = -kInf;
+        __syncwarp();
+        const float v0 = c_v[warp][lane], v1 = lane + 32 < cand ? c_v[warp][(lane + 32) % kCap] : -kInf;
+        int r0 = 0, r1 = 0;
+        for (int j = 0; j < cand; j += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(&c_v[warp][j]);
+            r0 += (o.x > v0) + (o.y > v0) + (o.z > v0) + (o.w > v0);
+            r1 += (o.x > v1) + (o.y > v1) + (o.z > v1) + (o.w > v1);
+        }
+        bool in0 = r0 < a.k, in1 = lane + 32 < cand && r1 < a.k;
+        const uint32_t ranks = __reduce_or_sync(kAll, (in0 ? 1u << r0 : 0u) | (in1 ? 1u << r1 : 0u));
+        const int count = __popc(__ballot_sync(kAll, in0)) + __popc(__ballot_sync(kAll, in1));
+        if (count != a.k || __popc(ranks) != a.k) {   // ties, as above
+            r0 = r1 = 0;
+            for (int j = 0; j < cand; ++j) {
+                const float o = c_v[warp][j];
+                r0 += o > v0 || (o == v0 && j < lane);
+                r1 += o > v1 || (o == v1 && j < lane + 32);
+            }
+            in0 = r0 < a.k;
+            in1 = lane + 32 < cand && r1 < a.k;
+        }
+        if (in0) c_win[warp][r0] = (uint8_t)lane;
+        if (in1) c_win[warp][r1] = (uint8_t)(lane + 32);
+        __syncwarp();
+        if (lane < a.k) {
+            const float2 se = c_se[warp][c_win[warp][lane]];
+            slot = lane;
+            cs = se.x;
+            ce = __float_as_int(se.y);
+        }
     }
-    if (!done && cand <= 32) {
-        for (int j = 0; j < a.k; ++j) {   // candidates are in index order: the lowest lane of the equals
+    if (P == 1) {   // k rounds over the lanes, which hold the experts in index order
+        for (int j = 0; j < a.k; ++j) {
             const float top = warp_max(cv);
             if (lane == __ffs(__ballot_sync(kAll, cv == top)) - 1) {
                 slot = j;
                 cv = -kInf;
-            }
-        }
-    } else if (!done && cand <= kCap) {
-        float qv[kCap / 32];
-#pragma unroll
-        for (int q = 0; q < kCap / 32; ++q) qv[q] = lane + 32 * q < cand ? c_v[warp][lane + 32 * q] : -kInf;
-        for (int j = 0; j < a.k; ++j) {
-            float best = qv[0];
-#pragma unroll
-            for (int q = 1; q < kCap / 32; ++q) best = fmaxf(best, qv[q]);
-            const float top = warp_max(best);
-            uint32_t at = kAll;   // the first of the equals
-#pragma unroll
-            for (int q = kCap / 32 - 1; q >= 0; --q)
-                if (qv[q] == top) at = lane + 32 * q;
-            at = __reduce_min_sync(kAll, at);
-#pragma unroll
-            for (int q = 0; q < kCap / 32; ++q)
-                if ((int)at == lane + 32 * q) qv[q] = -kInf;
-            if (lane == j) {
-                slot = j;
-                ce = __float_as_int(c_se[warp][at].y);
-                cs = c_se[warp][at].x;
-            }
-        }
-    } else if (!done) {
-        for (int j = 0; j < a.k; ++j) {
-            float best = v[0];
-#pragma unroll
-            for (int i = 1; i < P; ++i) best = fmaxf(best, v[i]);
-            const float top = warp_max(best);
-            const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
-            int e = 0;
-            float sc = 0.0f;
-            if (lane == from) {
-                bool found = false;
-#pragma unroll
-                for (int i = 0; i < P; ++i)
-                    if (!found && v[i] == top) {
-                        found = true;
-                        v[i] = -kInf;
-                        e = e0 + i;
-                        sc = kKeep ? s[i] : top;
-                    }
-            }
-            e = __shfl_sync(kAll, e, from);
-            sc = __shfl_sync(kAll, sc, from);
-            if (lane == j) {
-                slot = j;
-                ce = e;
-                cs = sc;
             }
         }
     }
@@ -348,6 +396,19 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(GateArgs a) {
             cs = fminf(fmaxf(l, -kInf), kMaxF) - m;
         }
         w = cs > kLowest ? (a.sigmoid ? sigmoid_score(cs) : softmax_term(cs) * inv) : 0.0f;
+    }
+    if (P > 1 && slow) {
+        uint32_t groups_kept = kAll;
+        if (kMode == kGroups) {   // bit g: a lane of group g still has a value that can be chosen
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < P; ++i) any |= v[i] > -kInf;
+            groups_kept = __reduce_or_sync(kAll, any ? 1u << g : 0u);
+        }
+        const Chosen c = gate_slow<T, P < 32 ? P : 32>(a, tok, groups_kept, m, inv);
+        slot = lane < a.k ? lane : -1;
+        ce = c.e;
+        w = c.s;
     }
     if (slot < 0) w = 0.0f;
     if (a.renormalise) {
@@ -374,14 +435,22 @@ cudaError_t launch_ps(const GateArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
 }
 
-// Samples: one a lane while k is at most 9/16 of the lanes that can hold a chosen expert (about 1.4 k candidates
-// then, 25 for k = 18 of 256), else four, whose rounds cost four times as much.
+// Samples: the fewest parts to a lane, of 1, 4 and 8, with which k is at most 9/16 of the samples (about 1.4 k candidates
+// then, 25 for k = 18 of 256); a round costs as many times as much.  All are candidates where they are at most 64 and k
+// is large.
 template <typename T, int P>
 cudaError_t launch_p(GateArgs a, cudaStream_t st) {
-    a.full = a.per == P << a.lane_shift && a.groups << a.lane_shift == 32;
-    if constexpr (P >= 8) {
-        const int lanes = a.groups > 1 ? a.group_topk << a.lane_shift : 32;
-        if (16 * a.k > 9 * lanes) return launch_ps<T, P, 4>(a, st);
+    const int lanes = (a.groups > 1 ? a.group_topk : 1) * ((a.per + a.lane_experts - 1) / a.lane_experts);   // that can matter
+    const auto enough = [&](int s) { return 16 * a.k <= 9 * lanes * ((a.lane_experts * s + P - 1) / P); };
+    a.full = a.lane_experts == P && a.per == P << a.lane_shift && a.groups << a.lane_shift == 32;
+    a.rounds = a.k;
+    if (P > 1 && lanes * a.lane_experts <= kMaxCand && 4 * a.k > lanes) a.rounds = 0;
+    else if constexpr (P >= 4) {
+        if (!enough(1)) {
+            if constexpr (P >= 8)
+                if (!enough(4)) return launch_ps<T, P, 8>(a, st);
+            return launch_ps<T, P, 4>(a, st);
+        }
     }
     return launch_ps<T, P, 1>(a, st);
 }
@@ -391,10 +460,14 @@ cudaError_t launch_t(GateArgs a, cudaStream_t st) {
     int lanes = 32;   // of a group: a power of two
     while (lanes * a.groups > 32) lanes /= 2;
     a.lane_shift = lanes == 32 ? 5 : lanes == 16 ? 4 : lanes == 8 ? 3 : lanes == 4 ? 2 : lanes == 2 ? 1 : 0;
-    const int need = (a.per + lanes - 1) / lanes;
-    // vector loads: every group and lane starts at a multiple of 16 bytes
-    a.vec = a.vec && (a.groups == 1 || a.per * sizeof(T) % 16 == 0);
-    a.bias_vec = reinterpret_cast<uintptr_t>(a.bias) % 16 == 0 && (a.groups == 1 || a.per % 4 == 0);
+    int need = (a.per + lanes - 1) / lanes;
+    // vector loads: every group and lane starts at a multiple of 16 bytes (lanes of at least four experts: a short one
+    // is loaded by elements anyway)
+    constexpr int kVec = 16 / (int)sizeof(T);
+    a.vec = a.vec && (a.groups == 1 || a.per % kVec == 0) && need >= kVec;
+    if (a.vec) need = (need + kVec - 1) / kVec * kVec;
+    a.lane_experts = need;
+    a.bias_vec = reinterpret_cast<uintptr_t>(a.bias) % 16 == 0 && (a.groups == 1 || a.per % 4 == 0) && need % 4 == 0;
     if (need <= 1) return launch_p<T, 1>(a, st);
     if (need <= 2) return launch_p<T, 2>(a, st);
     if (need <= 4) return launch_p<T, 4>(a, st);

@@ -751,6 +751,8 @@ struct GateArgs {
     int T, E, k;
     int groups, group_topk;
     int per, lane_shift;       // experts of a group, log2 of its lanes (set at launch)
+    int lane_experts;          // experts a lane holds, but at the end of a group (set at launch)
+    int rounds;                // of the bound's search (set at launch)
     bool sigmoid, group_max, renormalise, f16;
     bool vec, bias_vec;        // logits rows (bias) start at multiples of 16 bytes
     bool full;                 // every lane holds as many experts as it may (set at launch)
