@@ -245,6 +245,8 @@ def linear_workspace(cfg, device="cuda") -> torch.Tensor:
     n = moe_linear_workspace_bytes(cfg)
     if n == 0:
         raise MoEError("moe_linear_workspace_bytes", MOE_ERR_UNSUPPORTED)
+    if n <= 4096:
+        return torch.zeros(n, dtype=torch.uint8, device=device)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws

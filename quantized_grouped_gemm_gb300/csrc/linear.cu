@@ -24,7 +24,13 @@ __device__ __forceinline__ uint4 load8_words(const uint16_t* p, int left) {
     const uint32_t* q = reinterpret_cast<const uint32_t*>(p - odd);
     uint32_t w[5];
 #pragma unroll
-    for (int u = 0; u < 5; ++u) w[u] = 2 * u - odd < left && (u < 4 || odd) ? __ldg(q + u) : 0u;
+    for (int u = 0; u < 5; ++u) {   // word u holds elements 2u - odd and 2u + 1 - odd (the one before p among them)
+        w[u] = 0u;
+        if (u < 4 || odd) {
+            if (2 * u + 1 - odd < left) w[u] = __ldg(q + u);
+            else if (2 * u - odd < left) w[u] = __ldg(reinterpret_cast<const uint16_t*>(q + u));   // the row's last element
+        }
+    }
     uint32_t o[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -34,9 +40,9 @@ __device__ __forceinline__ uint4 load8_words(const uint16_t* p, int left) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The same for linear_rows.  kInside: 8 elements (16 without kVec) are known to remain, so that there is no branch and many loads go out
-// together.  kVec: p is 16-byte aligned; else the two aligned 16-byte blocks that hold the elements are loaded and shifted
-// together (in range: a row that does not start at such a block has the one before it in front of it).
+// The same for linear_rows.  kInside: 8 elements (16 without kVec) are known to remain, so that there is no branch and
+// many loads go out together.  kVec: p is 16-byte aligned; else the two aligned 16-byte blocks that hold the elements are
+// loaded and shifted together (in range: a row that does not start at such a block has the one before it in front of it).
 template <bool kVec, bool kInside>
 __device__ __forceinline__ uint4 load8(const uint16_t* p, int left) {
     if (!kInside) return load8_words(p, left);

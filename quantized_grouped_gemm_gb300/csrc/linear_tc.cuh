@@ -350,7 +350,13 @@ __global__ void __launch_bounds__(tc_threads(kGroups), 1)
             const int w0 = kGated ? n * kFeat + (rank ? a.l.N : 0) : n * kTN + (int)rank * kBRows;
             for (int kb = 0; kb < nkb; ++kb) {
                 if (!mbar_wait_warp(&sh->empty[s], ph, abort)) { ok = false; break; }
-                if (elect_one()) {
+#ifdef MOE_TEST_DROP_LINEAR_BLOCK
+                // timeout test only: both CTAs leave this block of the first tile out, so the issuer's wait on it never ends
+                const bool drop = i == 0 && kb == MOE_TEST_DROP_LINEAR_BLOCK;
+#else
+                constexpr bool drop = false;
+#endif
+                if (!drop && elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], 2 * kStage);
                     const uint32_t bar = map_to_rank(&sh->full[s], 0);
                     uint8_t* st = smem + s * kStage;
@@ -671,7 +677,12 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
             const int n0 = i % a.tiles_n * kLM, t0 = i / a.tiles_n * kTT;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait_warp(&sh.empty[s], ph, abort)) { ok = false; break; }
-                if (elect_one()) {
+#ifdef MOE_TEST_DROP_LINEAR_BLOCK
+                const bool drop = i == 0 && kb == MOE_TEST_DROP_LINEAR_BLOCK;   // as in linear_pair
+#else
+                constexpr bool drop = false;
+#endif
+                if (!drop && elect_one()) {
                     uint8_t* st = smem + s * kStage;
                     mbar_arrive_expect_tx(&sh.full[s], kStage);
 #pragma unroll
