@@ -20,7 +20,7 @@ namespace {
 constexpr int kGateWarps = 8;
 constexpr int kMaxCand = 64;   // candidates ranked by counting: up to two a lane
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr float kInf = __builtin_huge_valf(), kMaxF = 3.402823466e+38f;
+constexpr float kInf = __builtin_huge_valf(), kMaxF = 3.402823466e+38f, kMinNormal = 1.175494351e-38f;
 
 // How the choice values come about.
 enum GateMode {
@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     if (slot < 0) w = 0.0f;
     if (a.renormalise) {
         const float z = warp_sum(w);
-        w *= z > 0.0f ? __fdividef(a.scale, z) : 0.0f;
+        w *= z >= kMinNormal ? __fdividef(1.0f, z) : 0.0f;   // (1 / z stays finite; scale / z need not)
+        w *= a.scale;
     } else {
         w *= a.scale;
     }

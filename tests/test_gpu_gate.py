@@ -157,6 +157,26 @@ def test_gate_nan_and_infinities(score):
                 assert np.abs(w[6] - 0.25).max() <= W_RTOL
 
 
+@pytest.mark.parametrize("rest", [-86.0, -86.9])
+@pytest.mark.parametrize("ones", [1, 200])
+def test_gate_renormalises_the_smallest_scores(rest, ones):
+    """A bias that makes experts of scores near 2^-126 the chosen ones: their weights are scale / k each, as the
+    scores are equal, or 0 where the scores sum to less than 2^-126 (so count as 0), never infinite or NaN."""
+    E, k, scale = 256, 8, 300.0
+    logits = torch.full((1, E), rest, device="cuda")
+    logits[0, :ones] = 0.0
+    bias = torch.zeros(E, device="cuda")
+    bias[E - k:] = torch.arange(1, k + 1, device="cuda", dtype=torch.float32) * 4
+    idx, w = run_gate(logits, bias, 1, E, k, score="softmax", scale=scale)
+    assert idx[0].tolist() == list(range(E - 1, E - k - 1, -1))
+    total = k * np.exp(np.float64(rest)) / ones
+    assert abs(total / 2.0 ** -126 - 1) > 0.1        # far from the limit
+    want = scale / k if total >= 2.0 ** -126 else 0.0
+    # the scores are equal; the quotient, its product and the scale's round: 2^-22 + 2 * 2^-24.  A score below 2^-126 has
+    # fewer bits, the same ones in all eight
+    assert np.abs(w[0] - want).max() <= 2.0 ** -21 * scale, (w, want)
+
+
 def test_gate_nan_in_the_bias_switches_the_expert_off():
     l = torch.randn(50, 40, generator=torch.Generator().manual_seed(1))
     b = torch.zeros(40)
