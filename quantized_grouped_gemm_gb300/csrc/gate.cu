@@ -233,7 +233,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
             if (i >= cnt) v[i] = -kInf;
     }
 
-    if (kMode == kGroups && a.group_topk < a.groups) {
+    float lane_max = v[0];
+    bool kept = true;   // this lane's experts can be chosen from
+    if (kMode == kGroups) {
         // the two best of the lane, then of the group's lanes
         float v1 = v[0], v2 = -kInf;
 #pragma unroll
@@ -241,6 +243,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
             v2 = fmaxf(v2, fminf(v1, v[i]));
             v1 = fmaxf(v1, v[i]);
         }
+        lane_max = v1;
         for (int o = lpg >> 1; o >= 1; o >>= 1) {
             const float o1 = __shfl_xor_sync(kAll, v1, o), o2 = __shfl_xor_sync(kAll, v2, o);
             v2 = fmaxf(fmaxf(v2, o2), fminf(v1, o1));
@@ -250,11 +253,12 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         // make them more; then one group a round, the lowest lane (so the lowest group) first
         const float worth = g < a.groups ? fmaxf(a.group_max ? v1 : v1 + v2, -kMaxF) : -kInf;
         float left = worth, least = 0.0f;
+#pragma unroll 4
         for (int j = 0; j < a.group_topk; ++j) {
             least = warp_max(left);
             if (left == least) left = -kInf;
         }
-        bool kept = worth >= least && g < a.groups;
+        kept = worth >= least && g < a.groups;
         if (__builtin_expect(__popc(__ballot_sync(kAll, kept)) != a.group_topk << a.lane_shift, 0)) {
             kept = false;
             left = worth;
@@ -266,23 +270,23 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
                 }
             }
         }
-        if (!kept) {
+    } else {
 #pragma unroll
-            for (int i = 0; i < P; ++i) v[i] = -kInf;
-        }
+        for (int i = 1; i < P; ++i) lane_max = fmaxf(lane_max, v[i]);
     }
 
     // candidates: one a lane where a lane holds one expert anyway
     bool slow = false;
-    float cv = v[0], cs = kKeep ? s[0] : v[0];
+    float cv = kept ? v[0] : -kInf, cs = kKeep ? s[0] : v[0];
     int ce = e0, cand = 32;
     if (P > 1) {
         float h[S];
 #pragma unroll
         for (int q = 0; q < S; ++q) {
-            h[q] = v[q * (P / S)];
+            h[q] = S == 1 ? lane_max : v[q * (P / S)];
 #pragma unroll
-            for (int i = 1; i < P / S; ++i) h[q] = fmaxf(h[q], v[q * (P / S) + i]);
+            for (int i = 1; i < P / S && S > 1; ++i) h[q] = fmaxf(h[q], v[q * (P / S) + i]);
+            h[q] = kept ? h[q] : -kInf;
         }
         float bound = -kMaxF;
 #pragma unroll 4
@@ -296,6 +300,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
             for (int q = 0; q < S; ++q)
                 if (h[q] == top) h[q] = -kInf;
         }
+        if (!kept) bound = kInf;
         c_v[warp][lane] = -kInf;          // ranks are counted in fours
         int mine = 0;
 #pragma unroll
@@ -332,9 +337,17 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     int slot = -1;   // the chosen expert of this lane, if any: slot, index, score (or logit)
     if (P > 1 && cand <= 32) {
         int rank = 0;
-        for (int j = 0; j < cand; j += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(&c_v[warp][j]);
-            rank += (o.x > cv) + (o.y > cv) + (o.z > cv) + (o.w > cv);
+        if (cand <= 16) {   // two lanes to a candidate, each counts eight
+            const float x = c_v[warp][lane & 15];
+            const float4* half = reinterpret_cast<const float4*>(&c_v[warp][(lane & 16) >> 1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) rank += (half[j].x > x) + (half[j].y > x) + (half[j].z > x) + (half[j].w > x);
+            rank += __shfl_xor_sync(kAll, rank, 16);
+        } else {
+            for (int j = 0; j < cand; j += 4) {
+                const float4 o = *reinterpret_cast<const float4*>(&c_v[warp][j]);
+                rank += (o.x > cv) + (o.y > cv) + (o.z > cv) + (o.w > cv);
+            }
         }
         // no ties: the ranks of the candidates are 0 .. cand - 1
         if (__reduce_or_sync(kAll, lane < cand ? 1u << rank : 0u) != kAll >> (32 - cand)) {
@@ -399,11 +412,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     }
     if (P > 1 && slow) {
         uint32_t groups_kept = kAll;
-        if (kMode == kGroups) {   // bit g: a lane of group g still has a value that can be chosen
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < P; ++i) any |= v[i] > -kInf;
-            groups_kept = __reduce_or_sync(kAll, any ? 1u << g : 0u);
+        if (kMode == kGroups) {
+            groups_kept = __reduce_or_sync(kAll, kept ? 1u << g : 0u);
         }
         const Chosen c = gate_slow<T, P < 32 ? P : 32>(a, tok, groups_kept, m, inv);
         slot = lane < a.k ? lane : -1;
