@@ -177,6 +177,35 @@ def test_gate_renormalises_the_smallest_scores(rest, ones):
     assert np.abs(w[0] - want).max() <= 2.0 ** -21 * scale, (w, want)
 
 
+@pytest.mark.parametrize("E,k,groups,gk,with_bias,score,dt", [
+    (60, 6, 1, 1, False, "softmax", "f16"), (256, 8, 1, 1, False, "sigmoid", "f32"), (256, 8, 8, 4, True, "sigmoid", "f32"),
+    (296, 11, 8, 3, False, "sigmoid", "f16"), (512, 32, 1, 1, True, "softmax", "bf16"), (264, 18, 8, 6, False, "softmax", "f32"),
+    (1024, 24, 4, 2, True, "sigmoid", "bf16"), (1024, 32, 1, 1, False, "sigmoid", "f32"), (96, 20, 2, 1, False, "softmax", "f32")])
+def test_gate_among_many_equals(E, k, groups, gk, with_bias, score, dt):
+    """Most logits of a token are one value (or -inf): a few above it, none, more than k, a few below; the choice has to
+    be the largest values with the equals in index order."""
+    g = torch.Generator().manual_seed(5)
+    T = 64
+    logits = torch.zeros(T, E)
+    logits[1::4] = -torch.inf
+    for t in range(T):
+        above = [0, 1, k // 2, k - 1, k, k + 3, 40, 2][t % 8]
+        at = torch.randperm(E, generator=g)[:min(above + 9, E)]
+        logits[t, at[:above]] = (torch.arange(1, E + 1)[:len(at[:above])] % 13 + 1) / 8.0   # ties among them
+        logits[t, at[above:]] = -1.0
+    logits = logits.to(DT[dt])
+    bias = None
+    if with_bias:
+        bias = (torch.randint(0, 2, (E,), generator=g) * 0.5).float()
+    idx, w = run_gate(logits.cuda(), None if bias is None else bias.cuda(), T, E, k, score=score, groups=groups,
+                      group_topk=gk, scale=1.0)
+    want_idx, want_w, clear = reference(logits.double().numpy(), None if bias is None else bias.numpy(), E, k, score,
+                                        groups, gk, "top2", True, 1.0)
+    assert clear.all()
+    assert np.array_equal(idx, want_idx)
+    assert np.abs(w - want_w).max() <= W_RTOL, np.abs(w - want_w).max()
+
+
 def test_gate_nan_in_the_bias_switches_the_expert_off():
     l = torch.randn(50, 40, generator=torch.Generator().manual_seed(1))
     b = torch.zeros(40)
