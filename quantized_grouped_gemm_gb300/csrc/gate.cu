@@ -10,6 +10,10 @@
 // values >= B can be chosen -- about 9 of 256 for k = 8.  Those are compacted through shared memory, and each
 // finds its rank by counting the ones above it (and, when the ranks turn out not to be a permutation, the equal ones
 // before it).  More than 64 candidates go to gate_slow.
+//
+// Measured: 65536 x 256 fp32 sigmoid scores with a bias in 8 groups, k = 8: 31.5 us = 2.3 TB/s of logits and choices, 534
+// instructions a token (90 % of the issue slots; 10.5 us would be the bytes); 4096 x 512 bf16, k = 10: 5.2 us; up to 512
+// tokens of 256: 2 us, a launch and one token's chain of dependent reductions.
 #include "moe_internal.cuh"
 
 #include <cuda_fp16.h>

@@ -8,6 +8,10 @@
 // consecutive columns 8q .. 8q+7 of a 32-column piece of its rows (one 16-byte load) and uses them as the
 // k indices the fragment layout gives it; the tokens' columns are read the same way.  The eight partial
 // sums go through shared memory and are added in warp order.
+//
+// Bound by the weights' way into the registers: few tokens leave no reuse, and a tile in shared memory would only add a
+// copy and a barrier.  Measured: 1 x 2048 x 2048 in bf16 2.6 us = 3.3 TB/s, which is the launch and two loads' latency;
+// 8 x 4096 x 2048 3.4 us = 4.9 TB/s (out of L2).
 #include <type_traits>
 
 #include "linear_common.cuh"
@@ -244,7 +248,8 @@ struct Realign {
     int rows;
 };
 
-// A thread writes 16 bytes.
+// A thread writes 16 bytes.  Bound by latency at the sizes where it matters: 333 x 777 x 1001 takes 8.8 us with it and
+// 6.3 where the rows are aligned.
 __global__ void __launch_bounds__(256) realign_rows(Realign r0, Realign r1, int K, int pieces) {
     pdl_wait();
     pdl_launch_dependents();
@@ -265,7 +270,8 @@ __global__ void __launch_bounds__(256) realign_rows(Realign r0, Realign r1, int 
 // weights stream from HBM, which the tensor-core kernels do at the full rate.
 bool linear_takes_rows(const LinearArgs& a) {
     if (a.T > kFewTokens) return false;
-    LinearArgs nominal = a;   // on 152 SMs whatever the device at hand: the workspace's size, asked for anywhere, rests on this
+    // on 152 SMs whatever the device at hand: the workspace's size, asked for anywhere, rests on this
+    LinearArgs nominal = a;
     nominal.num_sms = 152;
     const double bytes = 2.0 * a.rows * a.K, iterations = (a.K + 1023) / 1024;
     const bool vec = straight(a.w_stride) && straight(a.x_stride);

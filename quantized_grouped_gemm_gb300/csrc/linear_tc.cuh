@@ -282,6 +282,9 @@ __device__ __forceinline__ void finish_column(const LinearArgs& l, long long t0,
     }
 }
 
+// Bound by the tensor cores: a stage's 64 columns are 512 clocks of products for 32 KB a CTA, which L2 delivers just in
+// time.  Measured in bf16: 4096 x 8192 x 2048 74 us = 1.86 PFLOP/s; 16384 x 8192 x 2048 with silu 277-290 us = 1.9-2.0,
+// at the clock that the power limit leaves; 4096 x 2048 x 4096 41-43 us = 1.6 (128 tiles on 76 pairs).
 // kTN: weight rows of a tile (256, or 128 with fp32 outputs so that a thread's running sums fit its
 // registers); with kGated half of them are gate rows and half the up rows of the same features.  kGroups: warpgroups of
 // the epilogue.
@@ -598,6 +601,9 @@ struct FeatArgs {
     int ring;          // bytes of the operand ring (with slices: at least of a tile's partial sums)
 };
 
+// Bound by HBM where the weights are large (16 x 131072 x 2048: 82 us = 6.6 TB/s), else by its stages: 64 columns of a
+// 128 x 64 tile take 0.18 us whether one CTA runs or 128 (4096 x 256 x 2048, fp32 out: 9.5 us), and loading the weight rows
+// once for two or four CTAs by multicast changes nothing there (10.9 us, the cluster's barriers being extra).
 // Weight rows as the M side: lane = feature, column = token, so a warp stores 32 consecutive features of a
 // token at once whatever the alignment of y, and a tile costs as many token columns as there are tokens.
 // kTT: tokens of a tile.  kGated: a tile has 128 gate rows and the 128 up rows of the same features, each with
@@ -722,7 +728,8 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
                                 const uint64_t ad = sw128_desc(sa + u * kBlock + g * kLM * 128);
 #pragma unroll
                                 for (int k = 0; k < kLK / 16; ++k)
-                                    tc_mma_f16kind<false>(d + g * kTT, ad + 2 * k, bd + 2 * k, idesc, kb > f || u > 0 || k > 0);
+                                    tc_mma_f16kind<false>(d + g * kTT, ad + 2 * k, bd + 2 * k, idesc,
+                                                          kb > f || u > 0 || k > 0);
                             }
                         }
                         tc_commit(&sh.empty[s]);
@@ -744,7 +751,8 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
         const bool has_res = a.l.residual && S == 1;
         OutElem<kOutF32> res[kBlk] = {};
         if (has_res && first < tiles)
-            load_residual<kOutF32, kBlk>(a.l, (long long)(first / a.tiles_n) * kTT + half * kHalf, first % a.tiles_n * kLM + r, res);
+            load_residual<kOutF32, kBlk>(a.l, (long long)(first / a.tiles_n) * kTT + half * kHalf,
+                                         first % a.tiles_n * kLM + r, res);
         for (int i = first; i < tiles && ok; i += step) {
             const int n = i % a.tiles_n * kLM + r;
             const long long t0 = (long long)(i / a.tiles_n) * kTT + half * kHalf;
@@ -819,7 +827,8 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
                 const int to = (rank + q) % S;
 #pragma unroll
                 for (int g = 0; g < G; ++g)
-                    bulk_s2s(map_to_rank(inbound + (rank * G + g) * per * kLM, to), own + (g * kTT + to * per) * kLM, per * kLM * 4,
+                    bulk_s2s(map_to_rank(inbound + (rank * G + g) * per * kLM, to), own + (g * kTT + to * per) * kLM,
+                             per * kLM * 4,
                              map_to_rank(&sh.joined, to));
             }
         }
@@ -946,7 +955,8 @@ cudaError_t launch_pair(const LinearArgs& l, cudaStream_t st) {
 
 template <bool kF16, bool kOutF32, bool kGated, int kTT>
 cudaError_t launch_feat_tt(const LinearArgs& l, int slices, cudaStream_t st) {
-    constexpr int G = kGated ? 2 : 1, kBlock = G * kLM * 128 + kTT * 128, kSub = feat_sub(kBlock), kStage = kSub * kBlock, kPart = G * kTT * kLM * 4;
+    constexpr int G = kGated ? 2 : 1, kBlock = G * kLM * 128 + kTT * 128, kSub = feat_sub(kBlock), kStage = kSub * kBlock;
+    constexpr int kPart = G * kTT * kLM * 4;         // bytes of a slice's partial sums
     constexpr int kMost = 220 * 1024;   // the barriers are in static shared memory
     auto* kernel = linear_feat<kF16, kOutF32, kGated, kTT>;
     static std::atomic<bool> set[64];
