@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     constexpr int kCap = 32 * P < kMaxCand ? 32 * P : kMaxCand;
     __shared__ __align__(16) float c_v[kGateWarps][kCap];   // the candidates' values,
     __shared__ float2 c_se[kGateWarps][kCap];               // scores (or logits) and indices
-    __shared__ uint8_t c_win[kGateWarps][32];
+    __shared__ uint8_t c_win[kGateWarps][kMaxCand];
     // A candidate's score is kept where a lane holds few experts.  Else it is worked out again from the logit of the
     // chosen, so that the scores need no registers after the choice values (4096 x 512, k = 10 in bf16 with bias:
     // 5.8 against 6.9 us; one token of 256 experts 2.6 against 2.1 us, the reload's latency).  By logits the value
@@ -409,11 +409,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         }
         // no ties: the ranks of the candidates are 0 .. cand - 1
         if (__reduce_or_sync(kAll, lane < cand ? 1u << rank : 0u) != kAll >> (32 - cand)) {
-            rank = 0;   // ties: the candidates are in index order
-            for (int j = 0; j < cand; ++j) {
-                const float o = c_v[warp][j];
-                rank += o > cv || (o == cv && j < lane);
-            }
+            // ties: equals have one rank, and the candidates are in index order
+            rank += __popc(__match_any_sync(kAll, lane < cand ? rank : 64 + lane) & ((1u << lane) - 1u));
         }
         if (lane < cand && rank < a.k) slot = rank;
     } else if (P > 1 && !slow) {
@@ -431,12 +428,15 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         const uint32_t ranks = __reduce_or_sync(kAll, (in0 ? 1u << r0 : 0u) | (in1 ? 1u << r1 : 0u));
         const int count = __popc(__ballot_sync(kAll, in0)) + __popc(__ballot_sync(kAll, in1));
         if (count != a.k || __popc(ranks) != a.k) {   // ties, as above
-            r0 = r1 = 0;
-            for (int j = 0; j < cand; ++j) {
-                const float o = c_v[warp][j];
-                r0 += o > v0 || (o == v0 && j < lane);
-                r1 += o > v1 || (o == v1 && j < lane + 32);
-            }
+            c_win[warp][lane] = c_win[warp][lane + 32] = 0;   // by rank: how many of the first 32 have it
+            __syncwarp();
+            const uint32_t m0 = __match_any_sync(kAll, r0);
+            const uint32_t m1 = __match_any_sync(kAll, lane + 32 < cand ? r1 : 64 + lane);
+            c_win[warp][r0] = (uint8_t)__popc(m0);
+            __syncwarp();
+            if (lane + 32 < cand) r1 += c_win[warp][r1] + __popc(m1 & ((1u << lane) - 1u));
+            r0 += __popc(m0 & ((1u << lane) - 1u));
+            __syncwarp();
             in0 = r0 < a.k;
             in1 = lane + 32 < cand && r1 < a.k;
         }
