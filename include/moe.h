@@ -311,7 +311,8 @@ int moe_forward_decode_static(const moe_shape* shape, const uint16_t* x_dev, con
  * Scores below about exp(-87), 2^-126, count as 0.  With neither bias nor groups the logits themselves are compared, so
  * that scores which round to one fp32 number (sigmoids near 1) keep their order.
  * Ties, of experts and of groups, go to the lower index.  A NaN logit counts as -inf, +inf as
- * the largest finite number; a NaN choice value as -inf.  -inf switches an expert off: its score
+ * the largest finite number; a NaN choice value as -inf.  A bias of +inf puts its expert (and its group)
+ * before all finite choice values, one of -inf behind them.  -inf switches an expert off: its score
  * is 0.  A token whose k chosen scores sum to 0 (every expert switched off) gets the lowest
  * indices of equal choice values and weights of 0, renormalised or not. */
 typedef struct moe_gate_config {

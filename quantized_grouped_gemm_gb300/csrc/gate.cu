@@ -138,11 +138,12 @@ __device__ __noinline__ Chosen gate_slow(const GateArgs& a, long long tok, int e
         __syncwarp();
         if (lane < a.k) order[warp][rank] = (uint16_t)e;
     } else {
-        float last = kInf;
-        for (int slots = 0; slots < a.k;) {
+        float last = 0.0f;
+        // the first round looks at every value, +inf (an infinite bias) among them; a round takes one expert at least
+        for (int slots = 0, round = 0; slots < a.k && round < a.k; ++round) {
             float best = -kInf;
 #pragma unroll
-            for (int i = 0; i < P; ++i) best = fmaxf(best, v[i] < last ? v[i] : -kInf);
+            for (int i = 0; i < P; ++i) best = fmaxf(best, round == 0 || v[i] < last ? v[i] : -kInf);
             last = warp_max(best);
             int mine = 0;
 #pragma unroll
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         for (int i = 0; i < P; ++i) s[i] = sigmoid_score(s[i]);
     }
 
-    // choice values (at least -FLT_MAX, also for NaN); -inf marks what cannot be chosen
+    // choice values (at least -FLT_MAX, also for NaN; +inf with an infinite bias); -inf marks what cannot be chosen
     float v[P];
     if (kByScore) {
         if (a.bias) {
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
             for (int q = 0; q < S; ++q)
                 if (h[q] == top) h[q] = -kInf;
         }
-        const float least = kept ? bound : kInf;
+        const float least = kept ? bound : __int_as_float(0x7fffffff);   // (no value is >= NaN, +inf neither)
         c_v[warp][lane] = -kInf;          // ranks are counted in fours
         int mine = 0;
 #pragma unroll

@@ -214,6 +214,59 @@ def test_gate_nan_in_the_bias_switches_the_expert_off():
     assert not (idx == 7).any() and np.isfinite(w).all()
 
 
+def by_value(v, count):
+    """Order of v, largest first and equals by index, and whether no two different finite values that the first `count`
+    places rest on are within what a score's rounding (GAP) could swap."""
+    o = sorted(range(len(v)), key=lambda e: (-v[e], e))
+    near = any(0 < v[a] - v[b] <= GAP["softmax"] * 2 * abs(v[a]) for a, b in zip(o[:count], o[1:count + 1])
+               if np.isfinite(v[a]))
+    return o, not near
+
+
+@pytest.mark.parametrize("E,k,groups,gk", [
+    (20, 4, 1, 1), (20, 20, 1, 1), (60, 6, 1, 1), (64, 3, 1, 1), (100, 20, 4, 2), (256, 8, 1, 1), (256, 16, 1, 1),
+    (256, 32, 1, 1), (256, 8, 8, 4), (512, 32, 1, 1), (1000, 17, 4, 2), (1020, 32, 17, 9), (1024, 32, 1, 1),
+    (1024, 32, 32, 16)])
+@pytest.mark.parametrize("score,group_score", [("sigmoid", "top2"), ("softmax", "max")])
+def test_gate_infinite_biases(E, k, groups, gk, score, group_score):
+    """A bias of +inf forces its expert, however many there are (one, up to all, in more groups than are kept) and
+    wherever they lie; of these the lower indices come first.  -inf puts an expert behind the others."""
+    T, per = 4, E // groups
+    g = torch.Generator().manual_seed(E + k)
+    spread = torch.linspace(4.0, -4.0, E)              # distinct scores, thousandths apart
+    logits = torch.stack([spread, spread.flip(0), spread[torch.randperm(E, generator=g)],
+                          spread[torch.randperm(E, generator=g)]])
+    logits[3, ::3] = -np.inf
+    s = (torch.sigmoid(logits.double()) if score == "sigmoid" else torch.softmax(logits.double(), 1)).numpy()
+    one_per_group = (torch.arange(groups) * per + per // 2).tolist()
+    random = torch.randperm(E, generator=g).tolist()
+    clear = total = 0
+    for forced in ([0], [E - 1], random[:max(1, k - 1)], random[:k], range(E * 2 // 5), range(max(0, E - 16), E),
+                   range(E - max(1, k // 2)), range(E), one_per_group, one_per_group[1::2], range(E - per * (groups > 1))):
+        for behind in ([], random[E - E // 3:]):
+            bias = np.zeros(E)
+            bias[list(behind)] = -np.inf
+            bias[list(forced)] = np.inf
+            idx, w = run_gate(logits.cuda(), torch.tensor(bias, dtype=torch.float32).cuda(), T, E, k, score=score,
+                              groups=groups, group_topk=gk, group_score=group_score, renormalise=False)
+            for t in range(T):
+                v = s[t] + np.maximum(bias, -F32_MAX)  # (-inf counts as the lowest number: its sums stay numbers)
+                fine = True
+                if groups > 1:
+                    top = -np.sort(-v.reshape(groups, per), 1)
+                    order, fine = by_value(top[:, 0] if group_score == "max" else np.maximum(top[:, 0] + top[:, 1], -F32_MAX), gk)
+                    for dropped in order[gk:]:
+                        v[dropped * per:(dropped + 1) * per] = -np.inf
+                want, fine2 = by_value(v, k)
+                total += 1
+                assert len(set(idx[t])) == k and idx[t].min() >= 0 and idx[t].max() < E
+                if fine and fine2:
+                    clear += 1
+                    assert list(idx[t]) == want[:k], (t, list(forced)[:4], len(forced), len(behind))
+                    assert (np.abs(w[t] - s[t][want[:k]]) <= W_RTOL * s[t][want[:k]] + 1e-30).all()
+    assert clear > 0.9 * total
+
+
 def test_gate_unaligned_logits_and_zero_tokens():
     l = torch.randn(20, 257, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
     view = l[:, 1:]                       # rows at odd elements
