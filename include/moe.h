@@ -308,8 +308,9 @@ int moe_forward_decode_static(const moe_shape* shape, const uint16_t* x_dev, con
  *   the group_topk groups of the highest worth (group_score) can be chosen from;
  *   the k largest v are chosen (slots in rank order), weights w = s of the chosen (without the
  *   bias), renormalise: divided by their sum, then times scale.
- * Scores below about exp(-87), 2^-126, count as 0.  With neither bias nor groups the logits themselves are compared, so
- * that scores which round to one fp32 number (sigmoids near 1) keep their order.
+ * Scores below about exp(-87), 2^-126, count as 0 (by logits: those more than 87 below the largest, a sigmoid's below
+ * -87).  With neither bias nor groups the logits themselves are compared, so that scores which round to one fp32 number
+ * (sigmoids near 1, neighbouring logits far below a token's largest) keep their order.
  * Ties, of experts and of groups, go to the lower index.  A NaN logit counts as -inf, +inf as
  * the largest finite number; a NaN choice value as -inf.  A bias of +inf puts its expert (and its group)
  * before all finite choice values, one of -inf behind them.  -inf switches an expert off: its score

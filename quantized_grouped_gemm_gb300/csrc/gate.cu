@@ -28,8 +28,8 @@ constexpr float kInf = __builtin_huge_valf(), kMaxF = 3.402823466e+38f, kMinNorm
 
 // How the choice values come about.
 enum GateMode {
-    kLogits,        // neither bias nor groups: scores rise with the logits, which are compared themselves (those
-                    // whose score is 0 as equals); only the chosen experts' scores are computed
+    kLogits,        // neither bias nor groups: scores rise with the logits, which are compared themselves, before any
+                    // rounding (those whose score is 0 as equals); only the chosen experts' scores are computed
     kLogitsTotal,   // the same, with the softmax's sum over all experts (weights not renormalised)
     kScores,        // a bias: every expert's score
     kGroups         // groups, with or without a bias
@@ -89,16 +89,18 @@ __device__ __noinline__ Chosen gate_slow(const GateArgs& a, long long tok, int e
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const T* row = static_cast<const T*>(a.logits) + tok * a.stride;
     const bool by_score = a.bias || a.groups > 1;
-    const auto logit = [&](T l) { return fminf(fmaxf(logit_f32<T>(l, a.f16), -kInf), kMaxF) - m; };
+    const auto logit = [&](T l) { return fminf(fmaxf(logit_f32<T>(l, a.f16), -kInf), kMaxF); };
     const auto score = [&](float x) { return a.sigmoid ? sigmoid_score(x) : softmax_term(x) * inv; };
     float v[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         v[i] = -kInf;
         if (i < cnt) {
-            const float x = logit(row[e0 + i]);
+            const float l = logit(row[e0 + i]), x = l - m;
             if (a.bias) v[i] = fmaxf(score(x) + __ldg(a.bias + e0 + i), -kMaxF);
-            else v[i] = by_score ? score(x) : fmaxf(x, kLowest);
+            else if (by_score) v[i] = score(x);
+            else if (a.sigmoid) v[i] = fmaxf(x, kLowest);
+            else v[i] = x > kLowest ? (m > -kMaxF ? l : x) : -kMaxF;
         }
     }
     if (bound == -kInf) {   // the samples ran out among equals: the least of the lanes' largest values
@@ -170,7 +172,7 @@ __device__ __noinline__ Chosen gate_slow(const GateArgs& a, long long tok, int e
     Chosen c{0, 0.0f};
     if (lane < a.k) {
         c.e = order[warp][lane];
-        const float x = logit(row[c.e]);
+        const float x = logit(row[c.e]) - m;
         c.s = x > kLowest || by_score ? score(x) : 0.0f;
     }
     return c;
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     // A candidate's score is kept where a lane holds few experts.  Else it is worked out again from the logit of the
     // chosen, so that the scores need no registers after the choice values (4096 x 512, k = 10 in bf16 with bias:
     // 5.8 against 6.9 us; one token of 256 experts 2.6 against 2.1 us, the reload's latency).  By logits the value
-    // is the score's argument.
+    // is the logit.
     constexpr bool kKeep = kByScore && P <= 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long tok = (long long)blockIdx.x * kGateWarps + warp;
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     const int cnt = a.full ? P : g < a.groups ? max(0, min(a.lane_experts, a.per - sub * a.lane_experts)) : 0;
     const T* row = static_cast<const T*>(a.logits) + tok * a.stride + e0;
 
-    float s[P];   // logits (softmax: minus the largest), then with kByScore scores
+    float s[P];   // logits, then with kByScore scores
     constexpr int V = 16 / (int)sizeof(T) < P ? 16 / (int)sizeof(T) : P;   // elements of a vector load
     if (V * sizeof(T) == 16 && a.vec) {
 #pragma unroll
@@ -223,24 +225,30 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         for (int i = 0; i < P; ++i) s[i] = i < cnt ? logit_f32<T>(row[i], a.f16) : -kInf;
     }
 
-    float inv = 1.0f, m = 0.0f;
+    float inv = 1.0f, m = 0.0f, peak = 0.0f;   // softmax: the largest logit, and what the largest of s is
     if (!a.sigmoid) {
         m = s[0];
 #pragma unroll
         for (int i = 1; i < P; ++i) m = fmaxf(m, s[i]);   // fmaxf drops a NaN
         m = warp_max(m);
-        if (!(fabsf(m) <= kMaxF)) {   // +inf counts as the largest number; nothing left: every score is 0
-            m = m > 0.0f ? kMaxF : 0.0f;
+        peak = m;
+        if (!(m > -kMaxF && m <= kMaxF)) {   // +inf counts as the largest number; nothing left: every score is 0
+            const bool lowest = m == -kMaxF;
+            m = m > 0.0f ? kMaxF : lowest ? m : 0.0f;
+            peak = m;
 #pragma unroll
             for (int i = 0; i < P; ++i) s[i] = fminf(fmaxf(s[i], -kInf), kMaxF);
-        }
+            if (!kByScore && lowest) {   // -FLT_MAX will mark a score of 0
+                peak = 0.0f;
 #pragma unroll
-        for (int i = 0; i < P; ++i) s[i] -= m;
+                for (int i = 0; i < P; ++i) s[i] -= m;
+            }
+        }
         if (kMode != kLogits) {
             float z = 0.0f;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const float x = softmax_term(s[i]);
+                const float x = softmax_term(s[i] - peak);
                 z += x;
                 if (kByScore) s[i] = x;
             }
@@ -282,9 +290,12 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < P; ++i) v[i] = s[i];
         }
+    } else if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = fminf(fmaxf(s[i], kLowest), kMaxF);
     } else {
 #pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = s[i] = fminf(fmaxf(s[i], kLowest), kMaxF);
+        for (int i = 0; i < P; ++i) v[i] = s[i] - peak > kLowest ? s[i] : -kMaxF;
     }
     if (!a.full) {
 #pragma unroll
@@ -465,8 +476,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     if (!kKeep) {
         if (kByScore && slot >= 0) {
             const float l = logit_f32<T>(static_cast<const T*>(a.logits)[tok * a.stride + ce], a.f16);
-            cs = fminf(fmaxf(l, -kInf), kMaxF) - m;
+            cs = fminf(fmaxf(l, -kInf), kMaxF);
         }
+        cs -= kByScore ? m : peak;
         w = cs > kLowest ? (a.sigmoid ? sigmoid_score(cs) : softmax_term(cs) * inv) : 0.0f;
     }
     if (P > 1 && slow) {

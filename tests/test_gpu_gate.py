@@ -214,6 +214,64 @@ def test_gate_nan_in_the_bias_switches_the_expert_off():
     assert not (idx == 7).any() and np.isfinite(w).all()
 
 
+@pytest.mark.parametrize("E,k,crowd", [(3, 2, 2), (20, 6, 9), (60, 6, 40), (64, 3, 10), (256, 8, 30), (256, 16, 150),
+                                       (1000, 32, 60), (1024, 32, 700)])
+@pytest.mark.parametrize("renormalise", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_compares_the_logits_themselves(E, k, crowd, renormalise, score):
+    """Neighbouring fp32 numbers far below a token's largest logit, whose differences from it round to one number, and
+    sigmoids that round to 1: the order is that of the logits, to the last bit."""
+    T = 16
+    g = torch.Generator().manual_seed(E + crowd)
+    logits = torch.empty(T, E)
+    for t in range(T):
+        base, peak = [(1.0, 50.0), (5.0, 20.0), (-0.75, 64.0), (30.0, 30.5)][t % 4]
+        near = np.float32(base) + np.arange(crowd, dtype=np.float32) * np.spacing(np.float32(base))
+        row = np.full(E, base - 20.0, np.float32)
+        at = torch.randperm(E, generator=g).numpy()[:min(E, crowd + 1)]
+        row[at[1:]] = near[torch.randperm(crowd, generator=g).numpy()][:len(at) - 1]
+        row[at[0]] = peak
+        logits[t] = torch.from_numpy(row)
+    idx, w = run_gate(logits.cuda(), None, T, E, k, score=score, renormalise=renormalise)
+    l = logits.double().numpy()
+    want = np.argsort(-l, 1, kind="stable")[:, :k]
+    assert np.array_equal(idx, want)
+    s = 1.0 / (1.0 + np.exp(-l)) if score == "sigmoid" else np.exp(l - l.max(1, keepdims=True))
+    s = np.take_along_axis(s / (s.sum(1, keepdims=True) if score == "softmax" else 1.0), want, 1)
+    if renormalise:
+        s = s / s.sum(1, keepdims=True)
+    # W_RTOL is for |l| + |m| of 32, here up to 65
+    assert (np.abs(w - s) <= 2 * W_RTOL * s + 1e-30).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E,k", [(7, 5), (40, 6), (256, 8), (512, 32)])
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_gate_softmax_of_lowest_and_largest_logits(dt, E, k, renormalise):
+    """Masks of the type's lowest value: where they are all a token has they share its weight, before any -inf or NaN;
+    beside other logits they count as 0 like these.  Logits of the largest value likewise share."""
+    lo, hi = torch.finfo(DT[dt]).min, torch.finfo(DT[dt]).max
+    logits = torch.full((6, E), -np.inf)
+    logits[0] = lo
+    logits[1, E // 2:] = lo
+    logits[2, E - 2:] = lo
+    logits[2, 0] = float("nan")
+    logits[3, ::2] = lo
+    logits[3, E - 1] = 1.0
+    logits[4] = lo
+    logits[4, 1::3] = hi
+    logits[5, E - 2] = hi
+    idx, w = run_gate(logits.to(DT[dt]).cuda(), None, 6, E, k, renormalise=renormalise)
+    for t in range(6):
+        l = logits[t].numpy()
+        live = np.flatnonzero(l == np.nanmax(l))
+        want = (list(live) + [e for e in range(E) if e not in set(live)])[:k]
+        assert list(idx[t]) == want, t
+        n = min(k, len(live))
+        share = 1.0 / (n if renormalise else len(live))
+        assert np.abs(w[t][:n] - share).max() <= 2.0 ** -20 * share and (w[t][n:] == 0).all(), t
+
+
 def by_value(v, count):
     """Order of v, largest first and equals by index, and whether no two different finite values that the first `count`
     places rest on are within what a score's rounding (GAP) could swap."""
