@@ -91,7 +91,7 @@ typedef struct moe_expert_weights {
  *   topk_w    fp32  [T][k]   routing weights: softmax over the E logits renormalised
  *                            over the kept k (sum to 1 per token)
  *   counts    int32 [E]      rows routed to each expert
- *   offsets   int32 [E+1]    exclusive prefix scan of counts; offsets[E] = k*T
+ *   offsets   int32 [E+1]    exclusive prefix scan of counts; offsets[E] = k*T (less what moe_dispatch left out)
  *   perm      int32 [k*T]    group row p -> assignment t*k + j (rows of a group ascend in t)
  *   pos       int32 [T][k]   assignment -> group row (the inverse of perm)
  *   tiles     int32 [moe_max_tiles(T, tile_rows)][3]  block map (expert, first row, rows),
@@ -223,7 +223,7 @@ int moe_ffn_down(const moe_shape* shape, const moe_routing* routing, const void*
                  const moe_options* options, void* stream);
 
 /* Step a10: y [T][d] bf16 (round to nearest even).  Prefill: the sum, in fp32 and in a fixed
- * order, of each token's k weighted routed rows (found through routing.pos) and its shared
+ * order, of each token's k weighted routed rows (found through routing.pos, below routing.offsets[E]) and its shared
  * row, as moe_grouped_ffn left them.  Decode shapes: the fp32 token-order sum, which it then
  * clears: the decode kernels add into a sum that a fresh (zeroed) workspace or the previous
  * moe_combine / moe_forward left at zero. */
@@ -340,7 +340,8 @@ int moe_gate(const moe_gate_config* config, const void* logits_dev, const float*
  * (written by moe_gate or by any gate) -> counts, offsets, perm, pos, block map, and the token rows
  * gathered into expert order inside the workspace, as moe_route leaves them for moe_grouped_ffn.
  * x_dev [T][d] bf16.  A token's 8 experts must differ and lie in [0, 256): an index outside sets
- * MOE_STATUS_BAD_EXPERT and that row is left out.  moe_options.host_routing is not taken here
+ * MOE_STATUS_BAD_EXPERT and that row is left out of every sum (its pos is a row from offsets[256] on, which no
+ * assignment has).  moe_options.host_routing is not taken here
  * (MOE_ERR_UNSUPPORTED); the other options as in moe_route. */
 int moe_dispatch(const moe_shape* shape, const uint16_t* x_dev, const moe_routing* routing, void* workspace_dev,
                  size_t workspace_bytes, const moe_options* options, void* stream);

@@ -360,8 +360,8 @@ int moe_combine(const moe_shape* s, const moe_routing* rt, void* ws, size_t ws_b
     if (!is_decode(s, op) && ffn_rows_output(s->T, s->d, s->k, op.deterministic)) {
         // prefill: the down projection left weighted rows in Y; sum each token's rows
         if ((rc = check_routing(rt)) != MOE_OK) return rc;
-        e = launch_combine_rows(s->T, s->d, s->k, reinterpret_cast<const float*>(w8 + L.Y), rt->pos_dev, y,
-                                static_cast<cudaStream_t>(stream), &n);
+        e = launch_combine_rows(s->T, s->d, s->k, reinterpret_cast<const float*>(w8 + L.Y), rt->pos_dev,
+                                rt->offsets_dev + s->E, y, static_cast<cudaStream_t>(stream), &n);
     } else {
         e = launch_combine(s->T, s->d, reinterpret_cast<const float*>(w8 + L.acc), y, static_cast<cudaStream_t>(stream),
                            &n);

@@ -691,19 +691,23 @@ __global__ void __launch_bounds__(kTmThreads, 1)
     if (warp == kTmMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// y[t] = bf16( sum_j Y[pos[t k + j]] + Y[k T + t] ), j = 0..k-1 in order, then the shared row;
+// y[t] = bf16( sum_j Y[pos[t k + j]] + Y[k T + t] ), j = 0..k-1 in order, then the shared row; a slot whose pos is not
+// below *rows (the rows routed to experts, k T but where moe_dispatch left some out) adds nothing;
 // Y is [d/128][(k+1)T][128]; one thread per 4 columns of a token (16-byte loads, 8-byte store).
 __global__ void combine_rows_kernel(const float4* __restrict__ Y, const int32_t* __restrict__ pos,
-                                    uint2* __restrict__ y, int T, int d4, int k) {
+                                    const int32_t* __restrict__ rows, uint2* __restrict__ y, int T, int d4, int k) {
     const size_t n = (size_t)T * d4, tile4 = (size_t)(k + 1) * T * 32;   // float4s of a 128-column tile
     pdl_wait();
     pdl_launch_dependents();
+    const int nrows = __ldg(rows);
     for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
         const int t = (int)(i / d4), c = (int)(i % d4);
         const float4* Yc = Y + (size_t)(c >> 5) * tile4 + (c & 31);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int j = 0; j < k; ++j) {
-            const float4 v = __ldcs(Yc + (size_t)pos[(size_t)t * k + j] * 32);
+            const int p = pos[(size_t)t * k + j];
+            if (p >= nrows) continue;
+            const float4 v = __ldcs(Yc + (size_t)p * 32);
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
         const float4 v = __ldcs(Yc + ((size_t)k * T + t) * 32);
@@ -853,13 +857,13 @@ cudaError_t launch_down_tm(const FfnArgs& a, cudaStream_t st, unsigned long long
 }  // namespace moe
 
 namespace moe {
-cudaError_t launch_combine_rows(int T, int d, int k, const float* Y, const int32_t* pos, uint16_t* y, cudaStream_t st,
-                                unsigned long long* launches) {
+cudaError_t launch_combine_rows(int T, int d, int k, const float* Y, const int32_t* pos, const int32_t* rows, uint16_t* y,
+                                cudaStream_t st, unsigned long long* launches) {
     const size_t n = (size_t)T * (d / 4);
     const int blocks = (int)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192);
     *launches += 1;
     return launch_with_pdl(combine_rows_kernel, dim3(blocks), dim3(256), 0, st, reinterpret_cast<const float4*>(Y), pos,
-                           reinterpret_cast<uint2*>(y), T, d / 4, k);
+                           rows, reinterpret_cast<uint2*>(y), T, d / 4, k);
 }
 }  // namespace moe
 

@@ -737,8 +737,8 @@ struct FusedDecodeArgs {
     unsigned long long* trace; // tuning builds (MOE_TRACE) only
 };
 cudaError_t launch_gate_up_tm(const FfnArgs& a, cudaStream_t st, unsigned long long* launches);
-cudaError_t launch_combine_rows(int T, int d, int k, const float* Y, const int32_t* pos, uint16_t* y, cudaStream_t st,
-                                unsigned long long* launches);
+cudaError_t launch_combine_rows(int T, int d, int k, const float* Y, const int32_t* pos, const int32_t* rows, uint16_t* y,
+                                cudaStream_t st, unsigned long long* launches);
 cudaError_t launch_down_tm(const FfnArgs& a, cudaStream_t st, unsigned long long* launches);
 cudaError_t launch_decode_fused(const FusedDecodeArgs& a, cudaStream_t st, unsigned long long* launches);
 cudaError_t launch_pack(int E, int N, int K, const moe_q4& m, int pair_slot, int pair_count, uint8_t* dst,

@@ -1164,7 +1164,8 @@ namespace {
 // route_count: the per-block expert counts that route_scan reads, for a choice made elsewhere
 // (moe_dispatch).  One CTA per 32-token block, a thread per assignment; a token whose slots name
 // one expert twice counts once, as in route_scatter's bitmasks.  pos of an index outside [0, E)
-// (flagged by route_scatter) is set to 0, an existing row.  With the scan and the scatter, which
+// (flagged by route_scatter) is set to the last row, which no assignment has then: the sums leave
+// out rows from offsets[E] on.  With the scan and the scatter, which
 // are moe_route's, a dispatch takes 12.9 us for 512 tokens and 35.6 us for 4096 (d = 2048; the
 // gathered rows are 151 MB, 22 us of HBM).
 // ---------------------------------------------------------------------------------------
@@ -1179,7 +1180,7 @@ __global__ void __launch_bounds__(256) route_count(RouteArgs a) {
         const size_t q = (size_t)t * 8 + threadIdx.x % 8;
         const int e = a.topk_idx[q];
         if (e >= 0 && e < 256) atomicOr(&s_mask[e], 1u << (threadIdx.x / 8));
-        else a.pos[q] = 0;
+        else a.pos[q] = a.T * 8 - 1;
     }
     __syncthreads();
     reinterpret_cast<int32_t*>(a.ws + a.L.blk)[(size_t)blockIdx.x * 256 + threadIdx.x] = __popc(s_mask[threadIdx.x]);
@@ -1249,7 +1250,7 @@ __global__ void __launch_bounds__(1024) dispatch_one(RouteArgs a) {
             a.pos[tid] = p;
             a.perm[p] = tid;
         } else {
-            a.pos[tid] = 0;
+            a.pos[tid] = 7;   // no row of the token, as in route_count
         }
         if (tid == 0) *a.num_tiles = tiles;
     }

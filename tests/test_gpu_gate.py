@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import quantized_grouped_gemm_gb300 as moe
-from gpu_helpers import DeviceLayer, to_dev
+from gpu_helpers import DeviceLayer, assert_output_close, to_dev, y_to_f64
 from moe_workload import configs
 import oracle
 
@@ -436,6 +436,38 @@ def test_dispatch_flags_an_expert_out_of_range(T):
     assert int(rt.counts.sum()) == 8 * T - 2
     pos = rt.pos.cpu().numpy()
     assert pos.min() >= 0 and pos.max() < 8 * T
+
+
+@pytest.mark.parametrize("deterministic", [0, 1])
+@pytest.mark.parametrize("T", [1, 2, 40])
+@pytest.mark.parametrize("bad", ["some", "a token", "all"])
+def test_an_expert_out_of_range_is_left_out_of_the_sums(T, bad, deterministic):
+    """The layer's output is the sum over the valid slots, on a workspace that an earlier call has filled."""
+    shp, dl, x = layer(T)
+    lay = configs.make_layer(configs.custom_workload(f"gate_t{T}", T=T, d=shp.d, I=shp.I))
+    rng = np.random.RandomState(T)
+    idx = np.stack([rng.permutation(256)[:8] for _ in range(T)]).astype(np.int32)
+    w = rng.uniform(0.05, 0.3, (T, 8)).astype(np.float32)
+    off = np.zeros((T, 8), bool)
+    off[0, 5] = off[T - 1, 3] = True
+    if bad == "a token":
+        off[T // 2] = True
+    if bad == "all":
+        off[:] = True
+    opts = moe.options(deterministic=deterministic)
+    rt, ws = moe.Routing(T), moe.workspace(shp, opts)
+    rt.topk_w.copy_(torch.from_numpy(w))
+    xd = to_dev(x)
+    for leave_out in (False, True):
+        rt.topk_idx.copy_(torch.from_numpy(np.where(off & leave_out, rng.choice([-1, 256, 1 << 30], (T, 8)), idx)))
+        y = torch.empty(T, shp.d, dtype=torch.int16, device="cuda")
+        moe.moe_dispatch(shp, xd, rt, ws, opts)
+        moe.moe_grouped_ffn(shp, xd, rt, dl.packed_routed, dl.packed_shared, ws, opts)
+        moe.moe_combine(shp, rt, ws, y, opts)
+        rc, bits = moe.moe_read_status(ws)
+        assert (rc, bits) == ((moe.MOE_ERR_DEVICE_STATUS, moe.MOE_STATUS_BAD_EXPERT) if leave_out else (moe.MOE_OK, 0))
+        ref = oracle.moe_tokens(x, idx, np.where(off & leave_out, 0.0, w.astype(np.float64)), lay.routed, lay.shared)
+        assert_output_close(y_to_f64(y), ref, f"left out: {leave_out}")
 
 
 @pytest.mark.parametrize("T", [1, 100])
