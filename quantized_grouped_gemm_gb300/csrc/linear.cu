@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kRowsWarps = 8;
 constexpr int kRowsSlice = 128;   // columns of K a warp takes at a time
+constexpr int kRowsChunk = 4;     // slices of a warp summed in the tensor cores' accumulator for fp32 outputs: 512 columns
 
 // Elements p[0..7] of a row of which `left` remain (zeros beyond), from the aligned 4-byte words that hold them.
 __device__ __forceinline__ uint4 load8_words(const uint16_t* p, int left) {
@@ -75,7 +76,10 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
     else mma_bf16_16816(c, a0, a1, a2, a3, b0, b1);
 }
 
-template <bool kF16, bool kOutF32, bool kGated, int NT, bool kVec>
+// kLong: fp32 outputs of rows of which a warp has more than a chunk: a chunk's sums leave the accumulator and are added in
+// ordinary fp32 (see linear_tc.cuh).  A form of its own, as its loop costs the others registers (1 x 4096 x 2048: 3.95 against
+// 3.2 us, fewer CTAs of two launches side by side on an SM).
+template <bool kF16, bool kOutF32, bool kGated, int NT, bool kVec, bool kLong>
 __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows(LinearArgs a) {
     constexpr int S = kGated ? 2 : 1, kTok = 8 * NT, kPitch = 17;
     __shared__ float red[kRowsWarps][S][kTok * kPitch];
@@ -130,17 +134,26 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows(LinearArgs a) {
             }
         }
     };
-    for (int kc = warp * kRowsSlice; kc < a.K; kc += kRowsWarps * kRowsSlice) {
-        if (kc + kRowsSlice + (kVec ? 0 : 8) <= a.K) slice(kc, std::true_type{});
-        else slice(kc, std::false_type{});
+    int kc = warp * kRowsSlice;
+    for (bool first = true;; first = false) {
+        const int end = kLong ? min(a.K, kc + kRowsChunk * kRowsWarps * kRowsSlice) : a.K;
+        for (; kc < end; kc += kRowsWarps * kRowsSlice) {
+            if (kc + kRowsSlice + (kVec ? 0 : 8) <= a.K) slice(kc, std::true_type{});
+            else slice(kc, std::false_type{});
+        }
+        // the warp's sums, to where they meet the other warps' (a place is one thread's until the barrier)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float& r = red[warp][s][(8 * j + 2 * q + (i & 1)) * kPitch + g + 8 * (i >> 1)];
+                    r = !kLong || first ? acc[s][j][i] : r + acc[s][j][i];
+                    if (kLong) acc[s][j][i] = 0.0f;
+                }
+        if (!kLong || kc >= a.K) break;
     }
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                red[warp][s][(8 * j + 2 * q + (i & 1)) * kPitch + g + 8 * (i >> 1)] = acc[s][j][i];
     __syncthreads();
     for (int i = threadIdx.x; i < 16 * kTok; i += 32 * kRowsWarps) {
         const int r = i % 16, n = n0 + r;
@@ -163,8 +176,14 @@ template <bool kF16, bool kOutF32, bool kGated, bool kVec>
 cudaError_t launch_rows_nt(const LinearArgs& a, cudaStream_t st) {
     const int nt = a.T <= 8 ? 1 : 2;
     const dim3 grid((a.N + 15) / 16, (a.T + 8 * nt - 1) / (8 * nt)), block(32 * kRowsWarps);
-    if (nt == 1) return launch_with_pdl(linear_rows<kF16, kOutF32, kGated, 1, kVec>, grid, block, 0, st, a);
-    return launch_with_pdl(linear_rows<kF16, kOutF32, kGated, 2, kVec>, grid, block, 0, st, a);
+    if constexpr (kOutF32) {
+        if (a.K > kRowsChunk * kRowsWarps * kRowsSlice) {
+            if (nt == 1) return launch_with_pdl(linear_rows<kF16, true, kGated, 1, kVec, true>, grid, block, 0, st, a);
+            return launch_with_pdl(linear_rows<kF16, true, kGated, 2, kVec, true>, grid, block, 0, st, a);
+        }
+    }
+    if (nt == 1) return launch_with_pdl(linear_rows<kF16, kOutF32, kGated, 1, kVec, false>, grid, block, 0, st, a);
+    return launch_with_pdl(linear_rows<kF16, kOutF32, kGated, 2, kVec, false>, grid, block, 0, st, a);
 }
 
 template <bool kF16, bool kOutF32>

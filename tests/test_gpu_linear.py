@@ -126,6 +126,35 @@ def test_larger(T, N, K, out, act):
     check(T, N, K, "bf16", out, act, bias=True, residual=act == "none")
 
 
+@pytest.mark.parametrize("K", [512, 4096, 8192, 16384, 65536])
+@pytest.mark.parametrize("T,N,act", [(1, 64, "none"), (1, 2048, "none"), (1, 16, "swiglu"), (8, 256, "none"),
+                                     (1, 256, "swiglu"), (16, 100, "swiglu"), (200, 300, "none"), (200, 300, "swiglu")])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_fp32_sums_of_long_rows(T, N, act, K, dt):
+    """At most 512 products meet in the tensor cores' accumulator.  One product is 2^24 and the others 2^-5, which are
+    lost, 16 at a time and truncated, where they are added to it there, but not where they are first added to each other:
+    512 make 16, a multiple of the 2 that 2^24 counts in.  So at most 16 may be missing of the K / 32."""
+    big = 2.0 ** 24
+    rows = 2 * N if act == "swiglu" else N
+    for at in (0, 127, 128, K // 2, K - 1):
+        x = torch.ones(T, K, device="cuda", dtype=DT[dt])
+        w = torch.full((rows, K), 2.0 ** -5, device="cuda", dtype=DT[dt])
+        x[:, at] = 2.0 ** 12
+        w[:, at] = 2.0 ** 12
+        if act == "swiglu":                            # gates of 64, whose sigmoid is 1 in fp32
+            w[:N] = 0.0
+            w[:N, (at + 1) % K] = 64.0
+        cfg = moe.linear_config(T, N, K, dtype=DT[dt], out_dtype=torch.float32, activation=act)
+        y = torch.empty(T, N, device="cuda")
+        moe.moe_linear(cfg, x, w, None, None, y, moe.linear_workspace(cfg))
+        z = (y.double() if act == "none" else y.double() / 64.0) - big
+        # the quotient of the sigmoid and two products: 2^-22 of 2^24
+        slack = 0.0 if act == "none" else 4.0
+        lost = (K - 1) / 32 - z
+        assert lost.min().item() >= -slack - 2.0, (at, lost.min().item())   # (a multiple of 2: rounded by less than that)
+        assert lost.max().item() <= 16.0 + slack, (at, lost.max().item())
+
+
 @pytest.mark.parametrize("T", [4, 50, 600])
 def test_a_bad_row_stays_a_row(T):
     """NaN and infinity in one token's row, and in one weight row, reach that row and column only."""
