@@ -372,8 +372,8 @@ typedef struct moe_linear_config {
 size_t moe_linear_workspace_bytes(const moe_linear_config* config);
 
 /* bias_dev fp32 [N] ([2N] for MOE_ACT_SWIGLU) or null, residual_dev [T][N] of out_type or null.
- * Products are accumulated in fp32; for an fp32 y partial sums of at most 512 products go through
- * the tensor cores' accumulator before they are added in ordinary fp32.  Results do not depend on
+ * Products are accumulated in fp32; partial sums of at most 512 products (fp32 y) or 8192 (16-bit y)
+ * go through the tensor cores' accumulator, which truncates, before they are added in ordinary fp32.  Results do not depend on
  * the run (no atomics).  x, w and the workspace must be 16- and 256-byte aligned as
  * everywhere here, y and residual to 16 bytes, bias to 4.  y may be residual itself (same pointer and stride); else
  * y must not overlap an input. */

@@ -12,10 +12,11 @@
 //                 few, the 2..8 CTAs of a cluster take slices of K of one tile and add their fp32 partial sums
 //                 through distributed shared memory, in slice order, so that a small product uses most SMs.
 //
-// fp32 outputs: the tensor cores truncate when they add to the accumulator (about half a unit of 2^-23 of
-// the running sum at each 16-column step, always towards zero), so after chunk_blocks blocks the epilogue
-// takes the partial sum into registers and adds the next in ordinary fp32.  For 16-bit outputs that
-// error is far below the rounding of the output, and the whole of K stays in the accumulator.
+// The tensor cores truncate when they add to the accumulator (about half a unit of 2^-23 of the running sum at each
+// 16-column step, always towards zero), so after chunk_blocks blocks the partial sum leaves it and the next is added in
+// ordinary fp32.  fp32 outputs: every 512 columns (384 with SwiGLU), the sums held in registers.  16-bit outputs: every 8192
+// (an error of about 7.5e-6, a thirtieth of half a unit of fp16), the sums held in the other accumulator, which costs the
+// issuer a wait at each of these.
 #include <atomic>
 #include <type_traits>
 
@@ -24,9 +25,9 @@
 namespace moe {
 namespace {
 
-// Blocks summed in the accumulator for fp32 outputs: the relative error is about 5e-7 after 8 (in each of two factors with
-// SwiGLU, so 6 there).
-__host__ __device__ constexpr int chunk_blocks(bool gated) { return gated ? 6 : 8; }
+// Blocks summed in the accumulator.  fp32 outputs: the relative error is about 5e-7 after 8 (in each of two factors with
+// SwiGLU, so 6 there); it grows with their number.
+__host__ __device__ constexpr int chunk_blocks(bool out_f32, bool gated) { return !out_f32 ? 128 : gated ? 6 : 8; }
 // Threads: four warps (producer, issuer, TMEM, spare) and `groups` warpgroups of the epilogue, each with its share of
 // a tile's columns.  Four groups where the tile is wide: short K loops leave the time to the epilogue.
 __host__ __device__ constexpr int tc_threads(int groups) { return 128 * (1 + groups); }
@@ -149,6 +150,27 @@ __device__ __forceinline__ void add_chunk(uint32_t acc, float (&sum)[G * kCols],
             for (int j = 0; j < kCols; j += 8) tmem_st8(acc + g * kNext + j, &sum[g * kCols + j]);
         tmem_st_wait();
     }
+}
+
+// 16-bit outputs in several chunks: adds the sums so far, kCols columns (of each of G accumulators, kNext columns apart) at
+// `from`, to the chunk at `acc`.
+template <int G, int kCols, int kNext>
+__device__ __forceinline__ void add_sums(uint32_t from, uint32_t acc) {
+    constexpr int kB = kCols < 32 ? kCols : 32;
+#pragma unroll 1
+    for (int j = 0; j < G * kCols; j += kB) {
+        const int at = j < kCols ? j : j - kCols + kNext;
+        uint32_t p[kB], q[kB];
+        tmem_ld_cols<kB>(from + at, p);
+        tmem_ld_cols<kB>(acc + at, q);
+        tmem_ld_wait();
+        float v[kB];
+#pragma unroll
+        for (int u = 0; u < kB; ++u) v[u] = __uint_as_float(p[u]) + __uint_as_float(q[u]);
+#pragma unroll
+        for (int u = 0; u < kB; u += 8) tmem_st8(acc + at + u, &v[u]);
+    }
+    tmem_st_wait();
 }
 
 struct TcArgs {
@@ -295,6 +317,8 @@ __global__ void __launch_bounds__(tc_threads(kGroups), 1)
     constexpr int kBRows = kTN / 2;                          // weight rows a CTA holds
     constexpr int kABytes = kLM * 128, kBBytes = kBRows * 128, kStage = kABytes + kBBytes;
     constexpr int kBufs = 512 / kTN;                         // accumulators in TMEM
+    constexpr bool kChunks = kOutF32 || kGroups == 2;        // four groups only take short rows
+    static_assert(kOutF32 || kBufs == 2, "the sums of long rows go from one accumulator to the other");
     constexpr int kFeat = kGated ? kTN / 2 : kTN;            // outputs of a tile
     constexpr int kHalf = kFeat / kGroups;                   // outputs a warpgroup handles
     constexpr int kPairStages = kGroups == 2 ? 6 : 5;
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(tc_threads(kGroups), 1)
     const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
     const int tiles = a.tiles_m * a.tiles_n;
-    const int nkb = a.nkb, chunk = kOutF32 ? chunk_blocks(kGated) : nkb, nch = (nkb + chunk - 1) / chunk;
+    const int nkb = a.nkb, chunk = kChunks ? chunk_blocks(kOutF32, kGated) : nkb, nch = kChunks ? (nkb + chunk - 1) / chunk : 1;
     int* status = reinterpret_cast<int*>(a.l.ws);
     volatile int* abort = &sh->abort;
 
@@ -442,11 +466,16 @@ __global__ void __launch_bounds__(tc_threads(kGroups), 1)
                 tc_fence_after();
                 if constexpr (kOutF32) {
                     if (nch > 1) add_chunk<kGated ? 2 : 1, kHalf, kFeat>(cols + buf * kTN, sum, c == 0, c == nch - 1);
+                } else if constexpr (kChunks) {
+                    if (c > 0) add_sums<kGated ? 2 : 1, kHalf, kFeat>(cols + (buf ^ 1) * kTN, cols + buf * kTN);
                 }
-                if (c < nch - 1) {   // (the last accumulator is released below)
+                // an accumulator whose sums have gone on (the last one is released below)
+                if (kOutF32 ? c < nch - 1 : c > 0) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote_release(&sh->acc_empty[buf], 0);
+                    if (lane == 0) mbar_arrive_remote_release(&sh->acc_empty[kOutF32 ? buf : buf ^ 1], 0);
+                }
+                if (c < nch - 1) {
                     if (++buf == kBufs) { buf = 0; fph ^= 1; }
                 }
             }
@@ -620,6 +649,7 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
     constexpr int kBufs = 2 * kAcc <= 512 ? 2 : 1;
     constexpr int kTmem = kBufs * kAcc <= 32 ? 32 : kBufs * kAcc;
     static_assert((kTmem & (kTmem - 1)) == 0 && kTmem <= 512, "TMEM columns");
+    static_assert(kOutF32 || kBufs == 2, "the sums of long rows go from one accumulator to the other");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     __shared__ FeatSmem sh;
@@ -633,7 +663,7 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
     const int first = S > 1 ? blockIdx.x / S : blockIdx.x, step = S > 1 ? INT32_MAX / 2 : (int)gridDim.x;
     const int tiles = a.tiles_n * a.tiles_t;
     const int kb0 = (int)((long long)a.nkb * rank / S), kb1 = (int)((long long)a.nkb * (rank + 1) / S);
-    const int chunk = kOutF32 ? chunk_blocks(kGated) / kSub : a.nkb, nch = (kb1 - kb0 + chunk - 1) / chunk;
+    const int chunk = chunk_blocks(kOutF32, kGated) / kSub, nch = (kb1 - kb0 + chunk - 1) / chunk;
     int* status = reinterpret_cast<int*>(a.l.ws);
     volatile int* abort = &sh.abort;
 
@@ -764,11 +794,16 @@ __global__ void __launch_bounds__(tc_threads(feat_groups(kTT)), 1)
                 tc_fence_after();
                 if constexpr (kOutF32) {
                     if (nch > 1) add_chunk<G, kHalf, kTT>(cols + buf * kAcc, sum, c == 0, c == nch - 1);
+                } else if (c > 0) {
+                    add_sums<G, kHalf, kTT>(cols + (buf ^ 1) * kAcc, cols + buf * kAcc);
                 }
-                if (c < nch - 1) {   // (the last accumulator is released below)
+                // an accumulator whose sums have gone on (the last one is released below)
+                if (kOutF32 ? c < nch - 1 : c > 0) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+                    if (lane == 0) mbar_arrive(&sh.acc_empty[kOutF32 ? buf : buf ^ 1]);
+                }
+                if (c < nch - 1) {
                     if (++buf == kBufs) { buf = 0; fph ^= 1; }
                 }
             }

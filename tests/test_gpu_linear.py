@@ -155,6 +155,36 @@ def test_fp32_sums_of_long_rows(T, N, act, K, dt):
         assert lost.max().item() <= 16.0 + slack, (at, lost.max().item())
 
 
+@pytest.mark.parametrize("K", [8192, 8200, 16384, 40000, 65536])
+@pytest.mark.parametrize("T,N", [(1, 64), (8, 1000), (24, 2000), (200, 300), (600, 1024)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_16_bit_outputs_of_long_rows(T, N, act, K, dt):
+    """At most 8192 products meet in the tensor cores' accumulator.  As above, with one product of 2^10 and others of 2^-18,
+    16 of which are half of what 2^10 counts in; the residual takes the 2^10 off again, so that what is left shows in 16
+    bits.  8192 of the others make 2^-5, which is all that may be missing."""
+    at = K // 3
+    x = torch.full((T, K), 2.0 ** -9, device="cuda", dtype=DT[dt])
+    w = torch.full((2 * N if act == "swiglu" else N, K), 2.0 ** -9, device="cuda", dtype=DT[dt])
+    x[:, at], w[:, at] = 32.0, 32.0
+    unit = 1.0
+    if act == "swiglu":                                # gates of 32, whose sigmoid is 1 in fp32
+        unit = 32.0
+        w[:N] = 0.0
+        w[:N, at + 1] = 2.0 ** 14
+    r = torch.full((T, N), -unit * 2.0 ** 10, device="cuda", dtype=DT[dt])
+    y = torch.empty(T, N, device="cuda", dtype=DT[dt])
+    cfg = moe.linear_config(T, N, K, dtype=DT[dt], activation=act)
+    ws = moe.linear_workspace(cfg)
+    moe.moe_linear(cfg, x, w, None, r, y, ws)
+    assert moe.moe_read_status(ws)[0] == moe.MOE_OK
+    small = (K - 1) * 2.0 ** -18
+    lost = small - y.double() / unit
+    # the sum counts in 2^-13, once rounded and once truncated; the gate's quotient and products: 2^-22 of 2^10; y's rounding
+    slack = 2.0 ** -12 + (2.0 ** -12 if act == "swiglu" else 0.0) + ROUND[dt] * small
+    assert lost.min().item() >= -slack and lost.max().item() <= 2.0 ** -5 + slack, (lost.min().item(), lost.max().item())
+
+
 @pytest.mark.parametrize("T", [4, 50, 600])
 def test_a_bad_row_stays_a_row(T):
     """NaN and infinity in one token's row, and in one weight row, reach that row and column only."""
