@@ -41,9 +41,11 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
 // z Phi(z).  The upper tail of |z| is 0.5 exp(-z^2 / 2) times the scaled complementary error function, for which
 // a polynomial in t = 1 / (1 + 0.43 x), x = |z| / sqrt 2, was fitted here in 64 bits by least squares of the
 // relative error (1e-7 for x up to 9.3; 4e-7 with its terms in fp32), so that small values keep their digits.
+// Beyond |z| of about 13.2 the exponential is below 2^-126 and comes out as 0, from 20 on in either form: z is held there for
+// its argument only, so that z times the tail is 0 however large z is.
 template <bool kExact>
 __device__ __forceinline__ float gelu_f32(float z) {
-    const float x = fminf(fabsf(z), 13.0f), t = __fdividef(1.0f, fmaf(0.43f * 0.70710678f, x, 1.0f));
+    const float x = fminf(fabsf(z), 20.0f), t = __fdividef(1.0f, fmaf(0.43f * 0.70710678f, x, 1.0f));
     float p = 0.0737080984f;
     p = fmaf(p, t, -0.310374153f);
     p = fmaf(p, t, 0.383707111f);

@@ -185,6 +185,36 @@ def test_16_bit_outputs_of_long_rows(T, N, act, K, dt):
     assert lost.min().item() >= -slack and lost.max().item() <= 2.0 ** -5 + slack, (lost.min().item(), lost.max().item())
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("T", [3, 40, 600])
+def test_activations_far_from_zero(T, act, dt, out):
+    """Large arguments, given by the bias: 0 (or next to it) on the negative side, the argument itself on the other."""
+    z = torch.tensor([0.0, 8.0, 12.0, 12.99, 13.01, 13.1, 13.3, 14.0, 16.0, 19.9, 20.1, 30.0, 86.0, 100.0, 500.0, 6e4, 1e10, 1e20,
+                      1e36, 3e38], device="cuda")
+    z = torch.cat([z, -z])
+    N = z.numel()
+    cfg = moe.linear_config(T, N, 64, dtype=DT[dt], out_dtype=DT[out], activation=act)
+    x = torch.zeros(T, 64, device="cuda", dtype=DT[dt])
+    w = torch.zeros(N, 64, device="cuda", dtype=DT[dt])
+    y = torch.empty(T, N, device="cuda", dtype=DT[out])
+    moe.moe_linear(cfg, x, w, z, None, y, moe.linear_workspace(cfg))
+    z = z.double()
+    # forms that keep their digits in the tail (1 + tanh and torch's ndtr, which is 1 + erf, are 0 there)
+    v = {"silu": z * torch.sigmoid(z), "gelu": 0.5 * z * torch.special.erfc(-z * math.sqrt(0.5)),
+         "gelu_tanh": z * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))}[act]
+    assert not torch.isnan(y).any() and torch.equal(y, y[:1].expand(T, N))
+    y = y[0].double()
+    fits = v.abs() < torch.finfo(DT[out]).max
+    assert torch.equal(y[~fits], v[~fits].sign() * (float("inf") if out == "f16" else torch.finfo(DT[out]).max))
+    # a value's relative error: 2^-24 of the exponential's argument, up to 85 (gelu's square is rounded: 5e-6), for 16-bit
+    # outputs again of its product with log2 e (7e-6), 4e-7 of the fit; beside it half the least number of fp16 and 90 times
+    # (z) 2^-126, below which an exponential is 0
+    rel = 2.0 ** -15 if out != "f32" else 2.0 ** -17
+    tol = rel * v.abs() + ROUND[out] * v.abs() * 1.01 + 90 * 2.0 ** -126 + (2.0 ** -24 if out == "f16" else 0.0)
+    assert ((y - v).abs() <= tol)[fits].all(), ((y - v).abs() / tol)[fits].max().item()
+
+
 @pytest.mark.parametrize("T", [4, 50, 600])
 def test_a_bad_row_stays_a_row(T):
     """NaN and infinity in one token's row, and in one weight row, reach that row and column only."""
