@@ -313,8 +313,10 @@ int moe_forward_decode_static(const moe_shape* shape, const uint16_t* x_dev, con
  * (sigmoids near 1, neighbouring logits far below a token's largest) keep their order.
  * Ties, of experts and of groups, go to the lower index.  A NaN logit counts as -inf, +inf as
  * the largest finite number; a NaN choice value as -inf.  A bias of +inf puts its expert (and its group)
- * before all finite choice values, one of -inf behind them.  -inf switches an expert off: its score
- * is 0.  A token whose k chosen scores sum to 0 (every expert switched off) gets the lowest
+ * before all finite choice values, one of -inf behind them.  A logit of -inf makes an expert's score 0: without a
+ * bias it is behind every expert of a larger score, so switched off while k others are left; with a bias its choice
+ * value is the bias alone, and if that is among the k largest it takes a slot with a weight of 0.  (A bias of -inf
+ * keeps an expert out for all tokens.)  A token whose k chosen scores sum to 0 (every expert switched off) gets the lowest
  * indices of equal choice values and weights of 0, renormalised or not. */
 typedef struct moe_gate_config {
     int T, E, k;               /* 0 <= T <= 2^20, 1 <= E <= 1024, 1 <= k <= min(32, E) */

@@ -206,6 +206,23 @@ def test_gate_among_many_equals(E, k, groups, gk, with_bias, score, dt):
     assert np.abs(w - want_w).max() <= W_RTOL, np.abs(w - want_w).max()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(40, 6), (256, 8), (512, 10)])
+def test_gate_of_a_logit_of_minus_infinity_beside_a_bias(E, k, score):
+    """Such an expert has a score of 0, so its choice value is its bias: one that is among the k largest takes a slot, with a
+    weight of 0; without a bias it comes after every other expert; a bias of -inf keeps it out."""
+    T = 20
+    logits = torch.randn(T, E, generator=torch.Generator().manual_seed(E))
+    logits[:, 3] = logits[:, 7] = -np.inf
+    bias = torch.zeros(E)
+    bias[3], bias[5], bias[7] = 4.0, -np.inf, -np.inf
+    idx, w = run_gate(logits.cuda(), bias.cuda(), T, E, k, score=score, renormalise=False)
+    assert (idx[:, 0] == 3).all() and (w[:, 0] == 0).all() and (w[:, 1:] > 0).all()
+    assert not np.isin(idx, [5, 7]).any()
+    idx, w = run_gate(logits.cuda(), None, T, E, k, score=score)
+    assert not np.isin(idx, [3, 7]).any()
+
+
 def test_gate_nan_in_the_bias_switches_the_expert_off():
     l = torch.randn(50, 40, generator=torch.Generator().manual_seed(1))
     b = torch.zeros(40)
