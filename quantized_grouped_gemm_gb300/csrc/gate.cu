@@ -55,8 +55,10 @@ __device__ __forceinline__ float exp2_f32(float t) {
 constexpr float kLog2e = 1.44269504f;
 // Logits (softmax: less the largest) from which on a score is 0, next to the smallest normal number.
 constexpr float kLowest = -87.0f;
-// Scores.  The argument's rounding, 2^-24 |x log2 e|, is a relative error of at most 1e-6 of scores down to exp(-8)
-// of the largest (a sigmoid near 1 has a (1 - s)-th of it).  -inf and NaN (fmaxf drops it) give 0.
+// Scores.  The argument's rounding, 2^-24 |x log2 e| and a little from log2 e itself, is a relative error of 7.3e-8 |x|:
+// under 1e-6 for scores down to exp(-8) of the largest (a sigmoid near 1 has a (1 - s)-th of it), 6e-6 for those near
+// exp(-80), which only a bias can choose; a two-part product for every expert would cost three instructions on each.
+// -inf and NaN (fmaxf drops it) give 0.
 __device__ __forceinline__ float sigmoid_score(float l) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_f32(fmaxf(l, -__builtin_huge_valf()) * -kLog2e)));

@@ -177,6 +177,50 @@ def test_gate_renormalises_the_smallest_scores(rest, ones):
     assert np.abs(w[0] - want).max() <= 2.0 ** -21 * scale, (w, want)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [24, 60, 256, 512])
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_gate_accuracy_of_the_smallest_scores(score, E, renormalise):
+    """Experts far below the rest that a bias makes the chosen ones: a score's relative error grows with its logit's distance
+    from the largest (a sigmoid's own size), as the argument of its exponential is rounded: 2^-24 of x log2 e, and log2 e
+    by 2^-26.2 (7.3e-8 x together); beside it the hardware's exponential and quotient, sums and products: 8 times 2^-23."""
+    T, k = 64, 6
+    g = torch.Generator().manual_seed(E)
+    x = torch.linspace(1.0, 86.0, T)[:, None] + torch.rand(T, k, generator=g) * 0.5     # distances
+    logits = torch.zeros(T, E)
+    at = torch.randperm(E, generator=g)[:k]
+    if score == "softmax":
+        logits += 3.0 * torch.rand(T, E, generator=g) - 3.0
+        logits[:, (int(at[0]) + 1) % E if (int(at[0]) + 1) % E not in at else next(e for e in range(E) if e not in at)] = 0.0
+    logits[:, at] = -x
+    bias = torch.zeros(E)
+    bias[at] = 4.0 + 2.0 * torch.arange(k, 0, -1).float()
+    idx, w = run_gate(logits.cuda(), bias.cuda(), T, E, k, score=score, renormalise=renormalise)
+    assert (idx == at.numpy()).all()
+    l = logits.double()
+    s = (torch.sigmoid(l) if score == "sigmoid" else torch.softmax(l, 1))[:, at]
+    normal = (s.amin(1) > 2.0 ** -126).numpy()                # (a score below 2^-126 counts as 0)
+    assert normal.mean() > 0.9
+    s = (s / s.sum(1, keepdim=True) if renormalise else s).numpy()
+    # (renormalised: the sum's error too)
+    rel = (7.3e-8 * (x.numpy() + 0.5) + 8 * 2.0 ** -23) * (2 if renormalise else 1)
+    assert (np.abs(w - s) <= rel * s)[normal].all(), (np.abs(w - s) / (rel * s))[normal].max()
+
+
+def test_gate_of_many_tokens():
+    """2^20 tokens, and rows whose offsets pass 2^31 elements."""
+    T, E, k = 1 << 20, 16, 3
+    base = torch.randn(4096, E, generator=torch.Generator().manual_seed(3))
+    want = run_gate(base.cuda(), None, 4096, E, k, score="sigmoid")
+    for stride in (E, 2304):
+        buf = torch.empty(T, stride, dtype=torch.bfloat16 if stride > E else torch.float32, device="cuda")
+        buf[:, :E] = base.to(buf.dtype).cuda().repeat(T // 4096, 1)
+        if stride > E:
+            want = run_gate(base.to(buf.dtype).cuda(), None, 4096, E, k, score="sigmoid")
+        idx, w = run_gate(buf, None, T, E, k, stride=stride, score="sigmoid")
+        assert (idx.reshape(-1, 4096, k) == want[0]).all() and (w.reshape(-1, 4096, k) == want[1]).all()
+
+
 @pytest.mark.parametrize("E,k,groups,gk,with_bias,score,dt", [
     (60, 6, 1, 1, False, "softmax", "f16"), (256, 8, 1, 1, False, "sigmoid", "f32"), (256, 8, 8, 4, True, "sigmoid", "f32"),
     (296, 11, 8, 3, False, "sigmoid", "f16"), (512, 32, 1, 1, True, "softmax", "bf16"), (264, 18, 8, 6, False, "softmax", "f32"),
@@ -437,6 +481,25 @@ def test_dispatch_of_a_skewed_choice():
     pos = np.empty(8 * T, np.int64)
     pos[order] = np.arange(8 * T)
     assert np.array_equal(rt.pos.cpu().numpy().reshape(-1), pos)
+
+
+def test_dispatch_of_the_largest_chunk():
+    T, d = 65536, 256
+    shp = moe.shape(T, d, 256, 8, 128, 128)
+    x = torch.randint(-100, 100, (T, d), dtype=torch.int16, device="cuda")
+    idx = torch.rand(T, 256, device="cuda").argsort(1)[:, :8].int()
+    rt, ws = moe.Routing(T), moe.workspace(shp)
+    rt.topk_idx.copy_(idx)
+    rt.topk_w.fill_(0.125)
+    moe.moe_dispatch(shp, x, rt, ws)
+    assert moe.moe_read_status(ws)[0] == moe.MOE_OK
+    flat = idx.reshape(-1).long()
+    counts = torch.bincount(flat, minlength=256)
+    order = torch.sort(flat, stable=True).indices
+    assert torch.equal(rt.counts.long(), counts) and torch.equal(rt.perm.long(), order)
+    pos = torch.empty_like(order)
+    pos[order] = torch.arange(8 * T, device="cuda")
+    assert torch.equal(rt.pos.reshape(-1).long(), pos)
 
 
 @pytest.mark.parametrize("T", [1, 40])
