@@ -185,6 +185,22 @@ def test_16_bit_outputs_of_long_rows(T, N, act, K, dt):
     assert lost.min().item() >= -slack and lost.max().item() <= 2.0 ** -5 + slack, (lost.min().item(), lost.max().item())
 
 
+@pytest.mark.parametrize("T,N,K", [(1 << 20, 24, 64), ((1 << 20) - 1, 264, 40), (1, 1 << 20, 72), (17, (1 << 20) - 3, 64),
+                                   (300, 1 << 20, 64), (2, 24, 65536), (70, 40, 65535), (300, 264, 65536)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_largest_sizes(T, N, K, out):
+    """The ends of the accepted ranges: tokens, features, columns."""
+    check(T, N, K, "bf16", out, bias=True, residual=T * N < 1 << 27)
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,N,out", [(1 << 20, 16, "bf16"), ((1 << 20) - 5, 136, "f32")])
+def test_outputs_past_32_bits(T, N, out):
+    """Row offsets of y and of the residual above 2^31 elements."""
+    check(T, N, 64, "bf16", out, residual=True, rpad=2300 - N, ypad=2304 - N)
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
 @pytest.mark.parametrize("T", [3, 40, 600])
