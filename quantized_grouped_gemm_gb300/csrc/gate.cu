@@ -11,9 +11,9 @@
 // finds its rank by counting the ones above it (and, when the ranks turn out not to be a permutation, the equal ones
 // before it).  More than 64 candidates go to gate_slow.
 //
-// Measured: 65536 x 256 fp32 sigmoid scores with a bias in 8 groups, k = 8: 31.5 us = 2.3 TB/s of logits and choices, 534
-// instructions a token (90 % of the issue slots; 10.5 us would be the bytes); 4096 x 512 bf16, k = 10: 5.2 us; up to 512
-// tokens of 256: 2 us, a launch and one token's chain of dependent reductions.
+// Measured: 65536 x 256 fp32 sigmoid scores with a bias in 8 groups, k = 8: 33 us = 2.2 TB/s of logits and choices (31.6 where
+// these stay in L2), 523 instructions a token (86 % of the issue slots; 10.5 us would be the bytes); 4096 x 512 bf16 with a
+// bias, k = 10: 5.3 us; up to 512 tokens of 256: 2.0-2.7 us, a launch and one token's chain of dependent reductions.
 #include "moe_internal.cuh"
 
 #include <cuda_fp16.h>
@@ -78,7 +78,7 @@ template <> __device__ __forceinline__ float logit_f32<uint16_t>(uint16_t v, boo
 // all the experts that have it in index order, until k are chosen (there are at least k).  e0, cnt: the lane's experts
 // that can be chosen.  Lane j < k gets slot j's expert and score.
 // Not inlined, as the usual path has to fit the instruction cache, and the values are worked out again, as handing them
-// over costs the usual path registers (12875 x 728, k = 23 in bf16: 33.9 against 24.8 us).
+// over costs the usual path registers (12875 x 728, k = 23 in bf16: 33.9 against 24.8 us then, 26 now).
 struct Chosen {
     int e;
     float s;

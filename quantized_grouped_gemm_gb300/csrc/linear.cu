@@ -10,8 +10,9 @@
 // sums go through shared memory and are added in warp order.
 //
 // Bound by the weights' way into the registers: few tokens leave no reuse, and a tile in shared memory would only add a
-// copy and a barrier.  Measured: 1 x 2048 x 2048 in bf16 2.6 us = 3.3 TB/s, which is the launch and two loads' latency;
-// 8 x 4096 x 2048 3.4 us = 4.9 TB/s (out of L2).
+// copy and a barrier.  Measured: 1 x 2048 x 2048 in bf16 2.6 us = 3.2 TB/s, which is the launch and two loads' latency;
+// 8 x 4096 x 2048 3.5 us = 4.8 TB/s (out of L2); fp32 outputs 1 x 256 x 2048 2.4 us, 1 x 2048 x 16384 10.0 us = 6.7 TB/s out of
+// L2 and 20 us from HBM.
 #include <type_traits>
 
 #include "linear_common.cuh"
@@ -197,10 +198,10 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t st) {
 }  // namespace
 
 // Which kernel and tile: the least of an estimate in microseconds, fitted to runs of every form on products of
-// 1..4096 tokens (it is within about a tenth of them).  Per tile a CTA, or a pair, needs the longer of its K loop
+// 1..4096 tokens (of 86 sizes 68 take at most 1.05 times the best form's time, 81 at most 1.25, one 2.0).  Per tile a CTA, or a pair, needs the longer of its K loop
 // and its epilogue, as the two overlap; the launch, the last epilogue and joining slices come once.
 // Clusters of a size that run at a time with one CTA to an SM, as the device reports it: 152 SMs hold 76 of 2, 36
-// of 4 and 15 of 8.
+// of 4 and 15 of 8.  For the estimate only: more of them take turns.
 static int clusters_at_once(int size, int num_sms) {
     return size == 1 ? num_sms : size == 2 ? num_sms / 2 : size == 4 ? num_sms * 36 / 152 : num_sms * 15 / 152;
 }
@@ -267,7 +268,7 @@ struct Realign {
     int rows;
 };
 
-// A thread writes 16 bytes.  Bound by latency at the sizes where it matters: 333 x 777 x 1001 takes 8.8 us with it and
+// A thread writes 16 bytes.  Bound by latency at the sizes where it matters: 333 x 777 x 1001 takes 8.8-9.0 us with it and
 // 6.3 where the rows are aligned.
 __global__ void __launch_bounds__(256) realign_rows(Realign r0, Realign r1, int K, int pieces) {
     pdl_wait();

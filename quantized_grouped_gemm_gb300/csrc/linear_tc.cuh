@@ -305,8 +305,9 @@ __device__ __forceinline__ void finish_column(const LinearArgs& l, long long t0,
 }
 
 // Bound by the tensor cores: a stage's 64 columns are 512 clocks of products for 32 KB a CTA, which L2 delivers just in
-// time.  Measured in bf16: 4096 x 8192 x 2048 74 us = 1.86 PFLOP/s; 16384 x 8192 x 2048 with silu 277-290 us = 1.9-2.0,
-// at the clock that the power limit leaves; 4096 x 2048 x 4096 41-43 us = 1.6 (128 tiles on 76 pairs).
+// time.  Measured in bf16: 4096 x 8192 x 2048 74-76 us = 1.81-1.85 PFLOP/s; 16384 x 8192 x 2048 with silu 280-327 us = 1.7-2.0,
+// by the clock that the power limit leaves; 4096 x 2048 x 4096 43-46 us = 1.5-1.6 (128 tiles on 76 pairs); 4096 x 2048 x 16384,
+// two chunks, 153-166 us.
 // kTN: weight rows of a tile (256, or 128 with fp32 outputs so that a thread's running sums fit its
 // registers); with kGated half of them are gate rows and half the up rows of the same features.  kGroups: warpgroups of
 // the epilogue.
@@ -631,7 +632,7 @@ struct FeatArgs {
 };
 
 // Bound by HBM where the weights are large (16 x 131072 x 2048: 82 us = 6.6 TB/s), else by its stages: 64 columns of a
-// 128 x 64 tile take 0.18 us whether one CTA runs or 128 (4096 x 256 x 2048, fp32 out: 9.5 us), and loading the weight rows
+// 128 x 64 tile take 0.18 us whether one CTA runs or 128 (4096 x 256 x 2048, fp32 out: 9.6 us), and loading the weight rows
 // once for two or four CTAs by multicast changes nothing there (10.9 us, the cluster's barriers being extra).
 // Weight rows as the M side: lane = feature, column = token, so a warp stores 32 consecutive features of a
 // token at once whatever the alignment of y, and a tile costs as many token columns as there are tokens.
