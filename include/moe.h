@@ -378,8 +378,9 @@ size_t moe_linear_workspace_bytes(const moe_linear_config* config);
 
 /* bias_dev fp32 [N] ([2N] for MOE_ACT_SWIGLU) or null, residual_dev [T][N] of out_type or null.
  * Products are accumulated in fp32; partial sums of at most 512 products (fp32 y) or 8192 (16-bit y)
- * go through the tensor cores' accumulator, which truncates, before they are added in ordinary fp32.  Results do not depend on
- * the run (no atomics).  x, w and the workspace must be 16- and 256-byte aligned as
+ * go through the tensor cores' accumulator, which truncates, before they are added in ordinary fp32
+ * (so an fp32 y is off by about 5e-7 of its size, by up to 3e-6 where all products have one sign).
+ * Results do not depend on the run (no atomics).  x, w and the workspace must be 16- and 256-byte aligned as
  * everywhere here, y and residual to 16 bytes, bias to 4.  y may be residual itself (same pointer and stride); else
  * y must not overlap an input. */
 int moe_linear(const moe_linear_config* config, const void* x_dev, const void* w_dev, const float* bias_dev,
